@@ -46,6 +46,17 @@ _SIGS = {
     "fc_gguf_debug_bucketing": (ctypes.c_int, [_vp, _c_i64, _c_i64, _c_i64, _vp, _vp, _vp, _vp, _vp]),
     "fc_gguf_debug_int_dots": (ctypes.c_int, [_vp, _vp, _c_i64, _vp, _vp]),
     "fc_gguf_debug_weights": (ctypes.c_int, [_vp, _vp, _vp]),
+    # the serving operators (serving.py)
+    "fc_gguf_kv_create": (ctypes.c_int, [_c_i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _vp,
+                                         ctypes.POINTER(_vp)]),
+    "fc_gguf_kv_destroy": (ctypes.c_int, [_vp]),
+    "fc_gguf_kv_append": (ctypes.c_int, [_vp, _vp, _c_i64, ctypes.c_int, _vp, _c_i64, _vp, _c_i64, _c_i64, _vp, _vp,
+                                         ctypes.c_int, _vp, _vp, ctypes.c_int, ctypes.c_int, ctypes.c_float, _vp,
+                                         _c_i64, _vp]),
+    "fc_gguf_kv_attend": (ctypes.c_int, [_vp, _vp, _c_i64, ctypes.c_int, _c_i64, _vp, _vp, _c_i64, _vp, _c_i64,
+                                         _c_i64, _c_i64, ctypes.c_float, ctypes.c_int, _vp, _c_i64, _vp, _vp]),
+    "fc_gguf_logits": (ctypes.c_int, [_vp, _c_i64, ctypes.c_int, _c_i64, _c_i64, _vp, _c_i64, _vp, _vp, _vp, _vp, _vp,
+                                      _vp, _vp, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, ctypes.c_int, _vp]),
     "fc_gguf_strerror": (ctypes.c_char_p, [ctypes.c_int]),
 }
 

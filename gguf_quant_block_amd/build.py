@@ -33,7 +33,7 @@ CFLAGS = [
     "-Wno-unused-command-line-argument",
 ]
 SOURCES = ["fc_gguf_api.cpp", "layout.hip", "gemv.hip", "prefill.hip", "skinny.hip", "prefill_i8.hip",
-           "moe.hip", "dequant.hip"]
+           "moe.hip", "dequant.hip", "serving_api.cpp", "kv_append.hip", "attend.hip", "logits.hip"]
 CEIL_SOURCES = ["ceilings.hip"]
 
 
@@ -73,7 +73,7 @@ def build(jobs: int = 4, verbose: bool = False) -> str:
 
 
 # Host-side sanitizer build of the C-ABI layer (argument validation, handle
-# and workspace management): fc_gguf_api.cpp's host code with AddressSanitizer
+# and workspace management): the host code of the *_api.cpp files with AddressSanitizer
 # and UndefinedBehaviorSanitizer, linked with the regular kernel objects.  The
 # GPU code is built as usual (each sanitizer flag applies to the host pass
 # only).  Loaded by a process that preloads ASAN_RUNTIME.
@@ -93,17 +93,18 @@ def build_sanitized() -> str:
     """The host-sanitized library (after build(), whose kernel objects it reuses)."""
     san = os.path.dirname(SAN_LIB)
     os.makedirs(san, exist_ok=True)
-    objs = [os.path.join(BUILD, os.path.splitext(s)[0] + ".o") for s in SOURCES if s != "fc_gguf_api.cpp"]
+    objs = [os.path.join(BUILD, os.path.splitext(s)[0] + ".o") for s in SOURCES if not s.endswith("_api.cpp")]
     if not all(os.path.exists(o) for o in objs):
         build()
-    api = os.path.join(san, "fc_gguf_api.o")
-    cmd = [HIPCC, "-x", "hip", *CFLAGS, "-g", *SAN_HOST, "-c", os.path.join(CSRC, "fc_gguf_api.cpp"),
-           "-o", api]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("hipcc failed on the sanitized fc_gguf_api.cpp")
-    _link([api, *objs], SAN_LIB, [*SAN_HOST, "-shared-libsan", "-L/opt/rocm/lib", "-lrocblas",
+    apis = []
+    for src in (s for s in SOURCES if s.endswith("_api.cpp")):
+        apis.append(os.path.join(san, os.path.splitext(src)[0] + ".o"))
+        cmd = [HIPCC, "-x", "hip", *CFLAGS, "-g", *SAN_HOST, "-c", os.path.join(CSRC, src), "-o", apis[-1]]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError(f"hipcc failed on the sanitized {src}")
+    _link([*apis, *objs], SAN_LIB, [*SAN_HOST, "-shared-libsan", "-L/opt/rocm/lib", "-lrocblas",
                                   "-Wl,-rpath,/opt/rocm/lib"])
     return SAN_LIB
 

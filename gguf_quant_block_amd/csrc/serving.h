@@ -1,0 +1,144 @@
+// Shared by the serving operators (paged key/value cache, attention over it,
+// logits processing): kernel arguments, launchers and device helpers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "common.h"
+#include "internal.h"
+
+namespace fcg {
+
+typedef __bf16 bf16;
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+
+// Element types of the C-ABI (FC_GGUF_F16, FC_GGUF_BF16, FC_GGUF_F32).
+constexpr int DT_F16 = 0;
+constexpr int DT_BF16 = 1;
+constexpr int DT_F32 = 2;
+
+// The paged cache.  K page: [kv_heads][D/8][ps][8], V page: [kv_heads][ps/8][D][8]
+// elements.  Both are made of 16-byte pieces, 8 head dimensions of one token
+// (K) and 8 tokens of one head dimension (V): the two shapes in which the
+// matrix instructions' operands hold 8 consecutive values of the summed index
+// in one lane, for K.Q^T (summed over dimensions) and V^T.P^T (over tokens).
+struct KvPages {
+  void* k;
+  void* v;
+  int64_t pages;
+  int page_shift;      // log2(tokens per page), 4 .. 8
+  int kv_heads;
+  int head_dim;
+};
+
+struct AppendArgs {
+  KvPages kv;
+  const uint16_t* q;   // [T][q_heads][D], row strides in elements
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* q_out;
+  int64_t q_stride, k_stride, v_stride, o_stride;
+  const int32_t* slots;       // [T]
+  const int32_t* positions;   // [axes][T]
+  const float* inv_freq;      // [rot/2] or null: no rotation
+  const int32_t* pair_axis;   // [rot/2] or null: axis 0
+  int64_t T;
+  int q_heads, rot, axes, interleaved;
+  float rope_scale;
+  int tokens_per_wg, y_splits;
+};
+hipError_t launch_kv_append(const AppendArgs& a, int dtype, int num_cu, hipStream_t st);
+
+struct AttendArgs {
+  KvPages kv;
+  const uint16_t* q;
+  uint16_t* o;
+  float* lse;                 // [T][q_heads] or null
+  int64_t q_stride, o_stride;
+  const int32_t* cu_q;        // [seqs + 1]
+  const int32_t* kv_lens;     // [seqs]
+  const int32_t* table;       // [seqs][table_stride], table_w entries used
+  int64_t table_stride;
+  int64_t T;
+  int table_w, seqs, q_heads, group, max_q, window;
+  float scale_log2;           // scale * log2(e)
+  float* part;                // [splits][T * q_heads][D] partial sums
+  float* part_ml;             // [splits][T * q_heads][2] their maxima and totals
+  int splits;
+};
+struct AttendPlan {
+  int row_tiles;              // 16-row tiles per workgroup of the streaming kernel
+  int splits;
+};
+AttendPlan attend_plan(const AttendArgs& a, int num_cu);
+size_t attend_workspace_bytes(const AttendArgs& a, const AttendPlan& p);
+hipError_t launch_attend(const AttendArgs& a, const AttendPlan& p, int dtype, hipStream_t st);
+
+struct LogitsArgs {
+  const void* x;              // [rows][x_stride]
+  void* out;                  // [rows][o_stride]
+  int64_t rows, vocab, x_stride, o_stride;
+  const int32_t* tokens;      // [rows][tokens_stride] or null
+  int64_t tokens_stride;
+  const int32_t* lens;        // [rows]
+  const int32_t* prompt_lens; // [rows] or null: 0
+  const float* repetition;    // [rows] or null: 1
+  const float* frequency;     // [rows] or null: 0
+  const float* presence;      // [rows] or null: 0
+  const int32_t* bias_offsets;  // [rows + 1] or null
+  const int32_t* bias_ids;
+  const float* bias_values;
+  int64_t bias_count;         // entries of bias_ids and bias_values
+  const uint32_t* mask;       // [rows][mask_stride] words or null
+  int64_t mask_stride;
+};
+hipError_t launch_logits(const LogitsArgs& a, int in_dtype, int out_dtype, int num_cu, hipStream_t st);
+
+// ---- device helpers ----
+
+template <class E> struct Mat;
+template <> struct Mat<f16> {
+  typedef f16 x8 __attribute__((ext_vector_type(8)));
+  static constexpr uint32_t EXP1 = 0x04000400u;   // one exponent step in both halves of a dword
+  static __device__ __forceinline__ floatx4 mfma16(u32x4 a, u32x4 b, floatx4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ floatx16 mfma32(u32x4 a, u32x4 b, floatx16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
+  }
+};
+template <> struct Mat<bf16> {
+  typedef bf16 x8 __attribute__((ext_vector_type(8)));
+  static constexpr uint32_t EXP1 = 0x00800080u;
+  static __device__ __forceinline__ floatx4 mfma16(u32x4 a, u32x4 b, floatx4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ floatx16 mfma32(u32x4 a, u32x4 b, floatx16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
+  }
+};
+
+// two f32 -> two E in a dword, round to nearest even
+template <class E>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  typedef E x2 __attribute__((ext_vector_type(2)));
+  const x2 v = {(E)a, (E)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+template <class E>
+__device__ __forceinline__ float lo2f(uint32_t w) { return (float)__builtin_bit_cast(E, (uint16_t)w); }
+template <class E>
+__device__ __forceinline__ float hi2f(uint32_t w) { return (float)__builtin_bit_cast(E, (uint16_t)(w >> 16)); }
+
+// bits 15 and 31: whether the low and the high half are infinite or NaN
+// (an exponent of all ones carries into the sign's place when one step is added)
+template <class E>
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
+  return ((w & 0x7FFF7FFFu) + Mat<E>::EXP1) & 0x80008000u;
+}
+
+}  // namespace fcg

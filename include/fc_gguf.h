@@ -271,6 +271,139 @@ int fc_gguf_debug_bucketing(const int32_t* ids, int64_t P, int64_t E, int64_t BM
                             int32_t* pairs, int32_t* tiles, int32_t* ntiles, void* stream);
 int fc_gguf_debug_weights(fc_gguf_t h, void* dst, void* stream);
 
+/*
+ * ---- Serving operators: what stands between the FC layers of a decoder ----
+ *
+ * The paged key/value cache of one layer, rotation and append, attention of
+ * new tokens over the cache, and the processing of the output layer's logits.
+ * Conventions as above: 0 or a negative FC_GGUF_E* code, nothing launched on
+ * failure, asynchronous and stream-ordered.  Every C exception or allocation
+ * failure ends as a code.
+ */
+
+/* Element types. */
+#define FC_GGUF_F16  0
+#define FC_GGUF_BF16 1
+#define FC_GGUF_F32  2   /* logits only */
+
+typedef struct fc_gguf_kv* fc_gguf_kv_t;
+
+/*
+ * A handle over the cache memory of one layer, which stays the caller's: the
+ * caller allocates it, may copy whole pages in and out (in stream order), and
+ * frees it after fc_gguf_kv_destroy.
+ *   k_pages  device [pages][kv_heads][head_dim/8][page_size][8]
+ *   v_pages  device [pages][kv_heads][page_size/8][head_dim][8]
+ * elements of `dtype` (FC_GGUF_F16 or FC_GGUF_BF16, else EUNSUPPORTED), both
+ * 16-byte aligned: pieces of 8 dimensions of one token for keys, of 8 tokens
+ * of one dimension for values.  page_size: a power of two from 16 to 256.
+ * head_dim: 64, 96, 128 or 256 (else EUNSUPPORTED).  pages < 2^31,
+ * kv_heads <= 1024.  The memory need not be initialised.  The handle belongs
+ * to the device current now.  It owns a workspace for attention that is split
+ * over the keys, grown stream-ordered as an FC handle's is: one handle must
+ * not attend on two streams at once, and a graph is captured after a call of
+ * the largest sizes.
+ */
+int fc_gguf_kv_create(int64_t pages, int page_size, int kv_heads, int head_dim, int dtype, void* k_pages,
+                      void* v_pages, fc_gguf_kv_t* out);
+
+/* Frees the handle and its workspace (not the pages); NULL is accepted.
+ * Synchronises the handle's device if a workspace was in use. */
+int fc_gguf_kv_destroy(fc_gguf_kv_t h);
+
+/*
+ * Rotates the queries and keys of T tokens and appends keys and values to
+ * the cache.
+ *   q, k, v    device [T][q_heads | kv_heads | kv_heads][head_dim], 16-byte
+ *              aligned, row strides in elements, multiples of 8 and at least
+ *              a row long (so the three may be parts of one projection's rows)
+ *   slots      device i32[T]: page * page_size + place in the page, distinct;
+ *              a token whose slot is negative or past the cache is not
+ *              appended (its query is rotated all the same)
+ *   positions  device i32[axes][T]
+ *   inv_freq   device f32[rot_dim/2], or NULL: nothing is rotated (positions,
+ *              axes, pair_axis, rot_dim, interleaved, rope_scale are not read)
+ *   pair_axis  device i32[rot_dim/2]: the axis whose position turns a pair
+ *              (time, height, width for images and video), or NULL: axis 0.
+ *              An entry outside [0, axes) is taken as 0.
+ *   rot_dim    a multiple of 16 up to head_dim: the leading dimensions that
+ *              are rotated.  Pair j is (j, j + rot_dim/2) or, with
+ *              interleaved = 1, (2j, 2j + 1); its angle is
+ *              positions[pair_axis[j]][t] * inv_freq[j], taken in f64;
+ *              rope_scale multiplies sine and cosine.
+ *   q_out      device [T][q_heads][head_dim]; may be q itself with q's stride.
+ *              q_heads = 0: keys and values only (q and q_out are not read).
+ * q_out must not overlap k or v.  T == 0 is a no-op.  T <= 2^30.
+ */
+int fc_gguf_kv_append(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_heads, const void* k,
+                      int64_t k_stride, const void* v, int64_t v_stride, int64_t T, const int32_t* slots,
+                      const int32_t* positions, int axes, const float* inv_freq, const int32_t* pair_axis,
+                      int rot_dim, int interleaved, float rope_scale, void* q_out, int64_t q_out_stride,
+                      void* stream);
+
+/*
+ * Attention of new tokens over the cache: one token per sequence, a chunk of
+ * a prompt, or both in one call.
+ *   q, out       device [T][q_heads][head_dim] of the cache's type, 16-byte
+ *                aligned, row strides in elements, multiples of 8;
+ *                q_heads a multiple of kv_heads: query head x reads key head
+ *                x / (q_heads / kv_heads).  out must not overlap q.
+ *   cu_q         device i32[seqs + 1]: sequence s has rows cu_q[s] ..
+ *                cu_q[s + 1] of q, at most max_q of them (rows past max_q, or
+ *                of no sequence, are left unwritten)
+ *   kv_lens      device i32[seqs]: keys of each sequence, its new tokens among
+ *                them (append before attending).  Row i of n new tokens stands
+ *                at position p = kv_lens[s] - n + i and sees keys j <= p and,
+ *                with window > 0, j > p - window.
+ *   table        device i32[seqs][table_stride], table_width entries used:
+ *                the page of each page_size keys.  Keys past the table, and
+ *                keys of an entry outside [0, pages), take no part.
+ *   scale        finite and > 0 (1 / sqrt(head_dim) as a rule)
+ *   lse          device f32[T][q_heads] or NULL: the natural logarithm of the
+ *                sum of the exponentials, for joining with other keys
+ * A row that sees no key gets zeros and lse -inf; what masked keys and values
+ * hold (infinities and NaN included) changes nothing.  The keys are split
+ * over workgroups by max_q and table_width, which the host knows; lengths are
+ * read on the device, so a captured graph may be replayed with other lengths
+ * within them.  The order of summation depends on sizes only.  seqs <= 65535;
+ * table_width * page_size <= 2^30; T, seqs or max_q == 0 is a no-op.
+ */
+int fc_gguf_kv_attend(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_heads, int64_t T,
+                      const int32_t* cu_q, const int32_t* kv_lens, int64_t seqs, const int32_t* table,
+                      int64_t table_stride, int64_t table_width, int64_t max_q, float scale, int window,
+                      void* out, int64_t out_stride, float* lse, void* stream);
+
+/*
+ * Penalties, biases and a grammar's mask on logits.  For token v of a row, in
+ * f32 with one rounding to out's type, in this order:
+ *   x = x > 0 ? x / repetition : x * repetition   if v is among tokens[:len]
+ *   x -= frequency * n + (n > 0 ? presence : 0)   n: times v is among
+ *                                                 tokens[prompt_len:len]
+ *   x += bias                                     sum of v's list entries
+ *   x = -inf                                      if bit v of the mask is 0
+ *   x, out       device [rows][vocab] of dtype (F16, BF16 or F32) and
+ *                out_dtype (the same or F32), row strides in elements; out may
+ *                be x itself with the same stride and type
+ *   tokens       device i32[rows][tokens_stride], the prompt first, or NULL:
+ *                no penalties; ids outside [0, vocab) count for nothing.
+ *                lens i32[rows] (clamped to tokens_stride), prompt_lens
+ *                i32[rows] or NULL (0)
+ *   repetition, frequency, presence   device f32[rows] or NULL (1, 0, 0)
+ *   bias_offsets device i32[rows + 1] or NULL; row r's entries are bias_ids,
+ *                bias_values [bias_offsets[r], bias_offsets[r + 1]) of
+ *                bias_count; entries of one id are added in their order
+ *   mask         device u32[rows][mask_stride] or NULL: bit v % 32 of word
+ *                v / 32 allows token v
+ * rows <= 65535, vocab <= 2^30; rows == 0 is a no-op.  Runs on the current
+ * device.
+ */
+int fc_gguf_logits(const void* x, int64_t x_stride, int dtype, int64_t rows, int64_t vocab,
+                   const int32_t* tokens, int64_t tokens_stride, const int32_t* lens,
+                   const int32_t* prompt_lens, const float* repetition, const float* frequency,
+                   const float* presence, const int32_t* bias_offsets, const int32_t* bias_ids,
+                   const float* bias_values, int64_t bias_count, const uint32_t* mask, int64_t mask_stride,
+                   void* out, int64_t out_stride, int out_dtype, void* stream);
+
 /* Static description of an error code. */
 const char* fc_gguf_strerror(int code);
 
