@@ -1,0 +1,416 @@
+// Attention of chunks over the paged cache (many query rows for each key
+// head): tiles of rows against tiles of 64 keys in LDS.
+//
+// The rows of one key head are the tokens times the group of query heads that
+// share it, token by token; a wave has RB * 32 of them, a workgroup WAVES
+// times as many, and the keys and values of a tile are read once for all.
+//
+// S^T = K Q^T and O^T = V^T P^T on 32x32x16 matrix instructions: a lane holds
+// scores of one query row (column lane % 32).  Operand row 8a + 4h + b of the
+// first product is key 16 (a / 2) + 8h + 4 (a % 2) + b of 32, so that lane
+// half h ends with keys 16s + 8h .. 16s + 8h + 7, the elements of its operand
+// in the second product: the weights stay in their registers, and the maximum
+// needs one exchange between lanes.  The cache's 16-byte pieces are the
+// operands' shape, so a tile is a plain copy of pieces ([D/8][64] of keys,
+// [8][D] of values) whatever the page size, and every LDS read is a
+// contiguous 1024 bytes.
+//
+// The reference point m of a row's exponentials follows its maximum only when
+// that has grown by more than 2^LAZY: the weights stay below 2^LAZY (in range
+// of f16), and most tiles leave the sums as they are.
+#include <math.h>
+
+#include "attend.h"
+
+namespace fcg {
+namespace {
+
+constexpr int KT = 64;                           // keys of a tile
+constexpr float LAZY = 8.f;
+
+template <int D, int RB, int WAVES>
+struct TileCfg {
+  static constexpr int ROWS = WAVES * RB * 32;
+  static constexpr int KB = KT * D * 2;          // bytes of a tile's keys, and of its values
+  static constexpr int STAGE = 2 * KB;           // values of a tile, then keys of the next
+  static constexpr int STAGES = D <= 128 ? 3 : 2;
+  static constexpr int LDS = STAGES * STAGE + 16;
+  static_assert(STAGES == 3 || WAVES == 4, "a wave behind needs a third stage");
+  static constexpr int NI = D / 8 / WAVES;       // 1 KB pieces of keys per wave
+};
+
+// the workgroup's LDS accesses are done; loads from memory stay in flight
+__device__ __forceinline__ void half_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+template <class E, int D, int RB, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, WAVES == 4 && RB == 1 && D <= 128 ? 2 : 1) void attend_tile_kernel(AttendArgs a) {
+  using C = TileCfg<D, RB, WAVES>;
+  static_assert(D / 8 % WAVES == 0, "pieces per wave");
+  constexpr int KS = D / 16, DB = D / 32, NI = C::NI;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  int b = blockIdx.x;
+  const int hk = b % a.kv.kv_heads;
+  b /= a.kv.kv_heads;
+  const int split = b % a.splits;
+  b /= a.splits;
+  const int tiles = a.tiles;
+  RowTile t;
+  // the last rows see the most keys: they come first
+  if (!row_tile(a, b / tiles, hk, tiles - 1 - b % tiles, C::ROWS, a.stream_rows + 1, INT32_MAX, KT, t)) return;
+  int c0, c1;
+  split_range(t, split, a.splits, a.per_split, c0, c1);
+
+  const int ps = 1 << a.kv.page_shift;
+  const int64_t page_bytes = (int64_t)a.kv.kv_heads * ps * D * 2;
+  const uint8_t* kbase = (const uint8_t*)a.kv.k + (int64_t)hk * ps * D * 2;
+  const uint8_t* vbase = (const uint8_t*)a.kv.v + (int64_t)hk * ps * D * 2;
+  const int32_t* table = a.table + t.s * a.table_stride;
+
+  // rows of this wave
+  const int wrow0 = t.row0 + wave * RB * 32;
+  const int wlast = (wrow0 + RB * 32 < t.rows ? wrow0 + RB * 32 : t.rows) - 1;
+  const bool any_rows = wrow0 < t.rows;
+  const int wlo = t.base + wrow0 / a.group, whi = any_rows ? t.base + wlast / a.group : -1;
+
+  u32x4 q[RB][KS];
+  int pos[RB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i) {
+    const int row = wrow0 + i * 32 + r;
+    const bool there = row < t.rows;
+    const int tok = row / a.group;
+    pos[i] = there ? t.base + tok : -1;
+    const uint16_t* p = a.q + (t.q0 + tok) * a.q_stride + (hk * a.group + row - tok * a.group) * D + h * 8;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) q[i][k] = there ? *(const u32x4*)(p + k * 16) : (u32x4){0, 0, 0, 0};
+  }
+
+  floatx16 o[RB][DB];
+  float m[RB], l[RB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int x = 0; x < 16; ++x) o[i][d][x] = 0.f;
+  }
+
+  // page of key tok0 + lane, -1: none of the pool (its keys take no part)
+  auto page_at = [&](int tok0) -> int {
+    const int key = tok0 + lane;
+    if (key >= c1) return -1;
+    const int p = table[key >> a.kv.page_shift];
+    return (unsigned)p < (uint64_t)a.kv.pages ? p : -1;
+  };
+  // pieces of keys and of values on their way to LDS
+  u32x4 kst[NI], vst[NI];
+  auto load_k = [&](int tok0, int page) {
+    const uint8_t* kp = kbase + (page < 0 ? 0 : page) * page_bytes + ((tok0 + lane) & (ps - 1)) * 16;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) kst[i] = *(const u32x4*)(kp + (int64_t)(wave * NI + i) * ps * 16);
+  };
+  auto load_v = [&](int tok0, int page) {
+    page = page < 0 ? 0 : page;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      if constexpr (D % 64 == 0) {               // the wave's 64 pieces are of the same 8 keys
+        const int p = (wave * NI + i) * 64, k8 = p / D, d = p - k8 * D;
+        const uint8_t* vp = vbase + __builtin_amdgcn_readlane(page, k8 * 8) * page_bytes +
+                            (((tok0 + k8 * 8) & (ps - 1)) >> 3) * (D * 16) + d * 16;
+        vst[i] = *(const u32x4*)(vp + lane * 16);
+      } else {
+        const int p = (wave * NI + i) * 64 + lane, k8 = p / D, d = p - k8 * D;
+        vst[i] = *(const u32x4*)(vbase + __shfl(page, k8 * 8) * page_bytes + (((tok0 + k8 * 8) & (ps - 1)) >> 3) * (D * 16) +
+                                 d * 16);
+      }
+    }
+  };
+  int* const flag = (int*)(smem + C::STAGES * C::STAGE);   // some value was taken out
+  if (tid == 0) *flag = 0;
+  __syncthreads();
+  uint8_t* const mine = smem + (wave * NI * 64 + lane) * 16;
+  auto store = [&](int at, const u32x4* x) {     // at: where the tile's pieces begin
+#pragma unroll
+    for (int i = 0; i < NI; ++i) *(u32x4*)(mine + at + i * 1024) = x[i];
+  };
+  // the key of operand row r, in pieces
+  const int krow = ((r >> 4) & 1) * 16 + ((r >> 2) & 1) * 8 + ((r >> 3) & 1) * 4 + (r & 3);
+  const uint8_t* const kop = smem + C::KB + (h * KT + krow) * 16;
+  const uint8_t* const vop = smem + (h * D + r) * 16;
+
+  // ok: bit j: key tok0 + j has a page
+  // every row from position lo to hi sees every key of the tile: no mask
+  auto is_open = [&](int tok0, uint64_t ok, int lo, int hi) {
+    return ok == ~0ull && tok0 + KT - 1 <= lo && (a.window <= 0 || tok0 > hi - a.window);
+  };
+  // how many of the tile's keys 8x .. 8x + 7 are there (the first ones)
+  auto have = [&](int tok0, uint64_t ok, int x) -> int {
+    const int left = c1 - (tok0 + 8 * x);
+    return (ok >> (8 * x) & 1) ? (left < 8 ? left : 8) : 0;
+  };
+  // A masked key's weight is 0, which must not meet an infinite or NaN value:
+  // of tiles with masked keys those are stored as 0 and added at the end.
+  auto clean = [&](int tok0, uint64_t ok) {
+    if (is_open(tok0, ok, t.lo, t.hi)) return;
+    uint32_t bad = 0;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      vst[i] &= keep_keys(have(tok0, ok, ((wave * NI + i) * 64 + lane) / D));
+      bad |= take_nonfinite<E>(vst[i]);
+    }
+    if (bad) *flag = 1;
+  };
+
+  floatx16 sc[RB][2];                            // scores
+  u32x4 w[RB][4];                                // weights
+  auto scores = [&](int stage) {
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) sc[i][n][x] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const u32x4 kk = *(const u32x4*)(kop + stage + k * 2 * KT * 16 + n * 32 * 16);
+#pragma unroll
+        for (int i = 0; i < RB; ++i) sc[i][n] = Mat<E>::mfma32(kk, q[i][k], sc[i][n]);
+      }
+  };
+  auto weights = [&](int tok0, uint64_t ok) {
+    if (!is_open(tok0, ok, wlo, whi)) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int key0 = tok0 + s * 16 + 8 * h, n = have(tok0, ok, 2 * s + h);
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+          const int top = pos[i] - key0 < n ? pos[i] - key0 : n - 1;       // last key that the row sees
+          const int low = a.window > 0 ? pos[i] - a.window - key0 : -1;    // last before its window
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j > top || j <= low) sc[i][s >> 1][(s & 1) * 8 + j] = -INFINITY;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      float mx = fmaxf(sc[i][0][0], sc[i][1][0]);
+#pragma unroll
+      for (int x = 1; x < 16; ++x) mx = max3(mx, sc[i][0][x], sc[i][1][x]);
+      mx = fmaxf(mx, other_half(mx));
+      const float mn = mx * a.scale_log2;
+      if (__any(mn > m[i] + LAZY)) {             // (also where m is -inf and mn is not)
+        const float to = fmaxf(m[i], mn), ms = to == -INFINITY ? 0.f : to;
+        const float al = __builtin_amdgcn_exp2f(m[i] - ms);
+        m[i] = to;
+        l[i] *= al;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) o[i][d][x] *= al;
+      }
+      const float ms = m[i] == -INFINITY ? 0.f : m[i];
+      float sum = 0.f;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        float p[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          p[j] = __builtin_amdgcn_exp2f(fmaf(sc[i][s >> 1][(s & 1) * 8 + j], a.scale_log2, -ms));
+          sum += p[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[i][s][j] = pack2<E>(p[2 * j], p[2 * j + 1]);
+      }
+      l[i] += sum;
+    }
+  };
+  auto values = [&](int stage) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int d = 0; d < DB; ++d) {
+        const u32x4 v = *(const u32x4*)(vop + stage + (s * 2 * D + d * 32) * 16);
+#pragma unroll
+        for (int i = 0; i < RB; ++i) o[i][d] = Mat<E>::mfma32(v, w[i][s], o[i][d]);
+      }
+  };
+
+  // Stage n of the ring has the values of tile n - 1 and the keys of tile n.
+  // Of the loop's two halves one is vector work (weights), one matrix work.
+  // With 8 waves, waves 4 to 7 run one half behind waves 0 to 3, their
+  // neighbours on the SIMDs, so that one of the two kinds of work is always
+  // next to the other.  Stage n is stored in the first halves of tile n - 2,
+  // read in the second halves of tile n - 1, and free again two halves later.
+  if (c0 < c1) {
+    const bool behind = wave >= 4;
+    const int p0 = page_at(c0), p1 = page_at(c0 + KT);
+    int p2 = page_at(c0 + 2 * KT), p3 = page_at(c0 + 3 * KT);
+    uint64_t ok = __ballot(p0 >= 0), ok1 = __ballot(p1 >= 0), ok2 = __ballot(p2 >= 0);
+    load_k(c0, p0);
+    store(C::KB, kst);
+    load_v(c0, p0);
+    load_k(c0 + KT, p1);
+    clean(c0, ok);
+    store(C::STAGE, vst);
+    store(C::STAGE + C::KB, kst);
+    load_v(c0 + KT, p1);
+    load_k(c0 + 2 * KT, p2);
+    half_barrier();
+    scores(0);
+    if (behind || C::STAGES == 2) half_barrier();
+    int cur = C::STAGE, next = C::STAGES == 2 ? 0 : 2 * C::STAGE;
+    for (int tok0 = c0; tok0 < c1; tok0 += KT) {
+      // (past the last tile the loads are of keys without a page, never read)
+      clean(tok0 + KT, ok1);
+      store(next, vst);
+      store(next + C::KB, kst);
+      load_v(tok0 + 2 * KT, p2);
+      load_k(tok0 + 3 * KT, p3);
+      p2 = p3;
+      p3 = page_at(tok0 + 4 * KT);
+      weights(tok0, ok);
+      half_barrier();
+      values(cur);
+      scores(cur);
+      half_barrier();
+      cur = next;
+      next = next + C::STAGE == C::STAGES * C::STAGE ? 0 : next + C::STAGE;
+      ok = ok1;
+      ok1 = ok2;
+      ok2 = __ballot(p2 >= 0);
+    }
+    if (WAVES > 4 && !behind) half_barrier();
+  }
+
+  if (c0 < c1 && *flag) {                        // (all waves have passed the loop's last barrier)
+    for (int tok0 = c0; tok0 < c1; tok0 += KT) {
+      const int page = page_at(tok0);
+      const uint64_t ok = __ballot(page >= 0);
+      if (is_open(tok0, ok, t.lo, t.hi)) continue;
+      const int in_page = tok0 & (ps - 1);
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+          floatx16 c;
+#pragma unroll
+          for (int x = 0; x < 16; ++x) c[x] = 0.f;
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const int key0 = tok0 + s * 16 + 8 * h, n = have(tok0, ok, 2 * s + h);
+            const u32x4 one =
+                seen_ones<E>(pos[i] - key0 < n ? pos[i] - key0 : n - 1, a.window > 0 ? pos[i] - a.window - key0 : -1);
+            const int pg = __shfl(page, s * 16 + 8 * h);
+            const u32x4 v = *(const u32x4*)(vbase + (pg < 0 ? 0 : pg) * page_bytes +
+                                            ((((in_page + s * 16 + 8 * h) & (ps - 1)) >> 3) * D + d * 32 + r) * 16);
+            c = Mat<E>::mfma32(nonfinite_codes<E>(v & keep_keys(n)), one, c);
+          }
+#pragma unroll
+          for (int x = 0; x < 16; ++x) o[i][d][x] += nonfinite_sum(c[x]);
+        }
+    }
+  }
+
+  // rows out: through LDS, a wave's 32 rows at a time (the loop's last barrier
+  // has passed: no wave reads the tiles any more)
+#pragma unroll
+  for (int i = 0; i < RB; ++i) {
+    const float lt = l[i] + __shfl_xor(l[i], 32);
+    const int row = wrow0 + i * 32 + r;
+    const int tok = row / a.group, head = hk * a.group + row - tok * a.group;
+    const int64_t orow = (int64_t)(t.q0 + tok) * a.q_heads + head;
+    if (a.splits > 1) {
+      if (row < t.rows) {
+        const int64_t at = (int64_t)split * a.T * a.q_heads + orow;
+        if (h == 0) *(float2*)(a.part_ml + at * 2) = make_float2(m[i], lt);
+        if (c0 < c1) {
+          float* p = a.part + at * D + 4 * h;
+#pragma unroll
+          for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              *(floatx4*)(p + d * 32 + 8 * x) =
+                  (floatx4){o[i][d][4 * x], o[i][d][4 * x + 1], o[i][d][4 * x + 2], o[i][d][4 * x + 3]};
+        }
+      }
+      continue;
+    }
+    const float f = lt == 0.f ? 0.f : 1.f / lt;
+    // 16-byte chunk c of row r at place c ^ (r & SWZ) of the row, for the banks
+    constexpr int SWZ = D == 96 ? 3 : 7;
+    static_assert(WAVES * 32 * D * 2 <= C::STAGES * C::STAGE, "rows fit");
+    uint8_t* s = smem + wave * 32 * D * 2;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        uint2 z;
+        z.x = pack2<E>(o[i][d][4 * x] * f, o[i][d][4 * x + 1] * f);
+        z.y = pack2<E>(o[i][d][4 * x + 2] * f, o[i][d][4 * x + 3] * f);
+        *(uint2*)(s + r * (D * 2) + ((d * 4 + x) ^ (r & SWZ)) * 16 + h * 8) = z;
+      }
+    if (a.lse && h == 0 && row < t.rows) a.lse[orow] = lt == 0.f ? -INFINITY : (m[i] + log2f(lt)) * LN2;
+    // (within a wave: LDS operations complete in order)
+    __builtin_amdgcn_wave_barrier();
+    for (int x = lane; x < 32 * (D / 8); x += 64) {
+      const int rr = x / (D / 8), c = x - rr * (D / 8), row2 = wrow0 + i * 32 + rr;
+      if (row2 < t.rows) {
+        const int tok2 = row2 / a.group, head2 = hk * a.group + row2 - tok2 * a.group;
+        *(u32x4*)(a.o + (t.q0 + tok2) * a.o_stride + head2 * D + c * 8) =
+            *(const u32x4*)(s + rr * (D * 2) + (c ^ (rr & SWZ)) * 16);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+template <class E, int D, int RB, int WAVES>
+hipError_t tile_launch(const AttendArgs& args, hipStream_t st) {
+  using C = TileCfg<D, RB, WAVES>;
+  static std::atomic<uint64_t> raised{0};
+  const hipError_t e = raise_lds_limit((const void*)attend_tile_kernel<E, D, RB, WAVES>, C::LDS, raised);
+  if (e != hipSuccess) return e;
+  AttendArgs a = args;
+  a.tiles = (int)(((int64_t)a.max_q * a.group + C::ROWS - 1) / C::ROWS);
+  const int64_t wgs = (int64_t)a.tiles * a.seqs * a.splits * a.kv.kv_heads;
+  attend_tile_kernel<E, D, RB, WAVES><<<dim3((unsigned)wgs), WAVES * 64, C::LDS, st>>>(a);
+  return hipGetLastError();
+}
+
+template <class E, int D>
+hipError_t tile_d(const AttendArgs& a, const AttendPlan& p, hipStream_t st) {
+  if constexpr (D == 256) return tile_launch<E, D, 1, 4>(a, st);
+  else return p.tile_rows == 256 ? tile_launch<E, D, D == 64 ? 2 : 1, D == 64 ? 4 : D == 96 ? 4 : 8>(a, st) : tile_launch<E, D, 1, 4>(a, st);
+}
+
+template <class E>
+hipError_t tile_e(const AttendArgs& a, const AttendPlan& p, hipStream_t st) {
+  switch (a.kv.head_dim) {
+    case 64: return tile_d<E, 64>(a, p, st);
+    case 96: return tile_d<E, 96>(a, p, st);
+    case 128: return tile_d<E, 128>(a, p, st);
+    default: return tile_d<E, 256>(a, p, st);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_attend_tile(const AttendArgs& a, const AttendPlan& p, int dtype, hipStream_t st) {
+  return dtype == DT_F16 ? tile_e<f16>(a, p, st) : tile_e<bf16>(a, p, st);
+}
+
+}  // namespace fcg

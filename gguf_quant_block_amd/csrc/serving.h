@@ -66,13 +66,28 @@ struct AttendArgs {
   int64_t T;
   int table_w, seqs, q_heads, group, max_q, window;
   float scale_log2;           // scale * log2(e)
-  float* part;                // [splits][T * q_heads][D] partial sums
-  float* part_ml;             // [splits][T * q_heads][2] their maxima and totals
-  int splits;
+  float* part;                // partial sums, and
+  float* part_ml;             // their reference points and totals
+  int splits, per_split;      // splits of the tile kernel; keys of a split
+  int tiles;                  // row tiles of a sequence (tile kernel)
+  int stream_rows;            // most rows of a streamed sequence
+  int shares;                 // workgroups of the streaming kernel for each key head
+  bool whole;                 // each of them has a sequence of its own
+  uint32_t* arrived;          // [seqs][kv_heads] pieces of a sequence that are there; 0 between calls
+  int64_t counters;           // entries of `arrived`
+  bool fresh;                 // they are to be cleared first
 };
+// Sequences with at most AT_STREAM_ROWS rows (tokens times the group) for each
+// key head are the streaming kernel's, the others the tile kernel's; the
+// lengths are known on the device only, so where max_q allows both, both are
+// launched and a workgroup without rows of its kind ends at once.
+constexpr int AT_STREAM_ROWS = 32;
 struct AttendPlan {
-  int row_tiles;              // 16-row tiles per workgroup of the streaming kernel
-  int splits;
+  int stream_rows;            // most rows of a streamed sequence
+  int splits;                 // shares of the streaming kernel
+  bool whole;                 // of one sequence each
+  int tile_rows;              // rows of a workgroup of the tile kernel; 0: not launched
+  int tile_splits, tile_per;
 };
 AttendPlan attend_plan(const AttendArgs& a, int num_cu);
 size_t attend_workspace_bytes(const AttendArgs& a, const AttendPlan& p);
@@ -104,6 +119,7 @@ template <class E> struct Mat;
 template <> struct Mat<f16> {
   typedef f16 x8 __attribute__((ext_vector_type(8)));
   static constexpr uint32_t EXP1 = 0x04000400u;   // one exponent step in both halves of a dword
+  static constexpr uint32_t INF = 0x7C00u, ONE = 0x3C00u, TWO7 = 0x5800u, TWO14 = 0x7400u;
   static __device__ __forceinline__ floatx4 mfma16(u32x4 a, u32x4 b, floatx4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
   }
@@ -114,6 +130,7 @@ template <> struct Mat<f16> {
 template <> struct Mat<bf16> {
   typedef bf16 x8 __attribute__((ext_vector_type(8)));
   static constexpr uint32_t EXP1 = 0x00800080u;
+  static constexpr uint32_t INF = 0x7F80u, ONE = 0x3F80u, TWO7 = 0x4300u, TWO14 = 0x4680u;
   static __device__ __forceinline__ floatx4 mfma16(u32x4 a, u32x4 b, floatx4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
   }

@@ -18,8 +18,10 @@ struct fc_gguf_kv {
   int dtype = 0;
   int device = 0;
   int num_cu = 256;
-  void* ws = nullptr;           // split sums of the attention
+  void* ws = nullptr;           // the attention's counters, then its partial sums
   size_t ws_bytes = 0;
+  int64_t counters = 0;
+  bool fresh = false;           // the counters are to be cleared by the next call
 };
 
 namespace {
@@ -40,22 +42,31 @@ int check_kv_device(const fc_gguf_kv* h) {
   return dev == h->device ? FC_GGUF_OK : FC_GGUF_EDEVICE;
 }
 
-// Grows the workspace on the call's stream: released to and taken from the
-// device's stream-ordered pool, so that the growth waits for that stream only.
-int ensure_kv_ws(fc_gguf_kv* h, size_t bytes, hipStream_t st) {
-  if (bytes <= h->ws_bytes) return FC_GGUF_OK;
+size_t counter_bytes(int64_t counters) { return ((size_t)counters * 4 + 255) / 256 * 256; }
+
+// Grows the workspace (counters, then `bytes`) on the call's stream: released
+// to and taken from the device's stream-ordered pool, so that the growth waits
+// for that stream only.
+int ensure_kv_ws(fc_gguf_kv* h, int64_t counters, size_t bytes, hipStream_t st) {
+  if (counters <= h->counters && counter_bytes(h->counters) + bytes <= h->ws_bytes) return FC_GGUF_OK;
   if (fail_workspace()) return FC_GGUF_ENOMEM;
+  if (counters < h->counters) counters = h->counters;
+  if (counters < 1024) counters = 1024;
+  const size_t total = counter_bytes(counters) + bytes;
   if (h->ws) {
     const hipError_t e = hipFreeAsync(h->ws, st);
     h->ws = nullptr;
     h->ws_bytes = 0;
+    h->counters = 0;
     if (e != hipSuccess) return FC_GGUF_EHIP;
   }
-  if (hipMallocAsync(&h->ws, bytes, st) != hipSuccess) {
+  if (hipMallocAsync(&h->ws, total, st) != hipSuccess) {
     h->ws = nullptr;
     return FC_GGUF_ENOMEM;
   }
-  h->ws_bytes = bytes;
+  h->ws_bytes = total;
+  h->counters = counters;
+  h->fresh = true;
   return FC_GGUF_OK;
 }
 
@@ -167,6 +178,8 @@ int fc_gguf_kv_attend(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_hea
   if (!h || T < 0 || seqs < 0 || q_heads <= 0 || q_heads % h->kv.kv_heads || max_q < 0 || table_width < 0 ||
       table_stride < table_width || window < 0 || !(scale > 0.f) || !isfinite(scale))
     return FC_GGUF_EINVAL;
+  const float scale_log2 = (float)((double)scale * 1.4426950408889634074);
+  if (!isfinite(scale_log2) || window > kMaxTokens) return FC_GGUF_ERANGE;
   if (const int rc = check_kv_device(h); rc != FC_GGUF_OK) return rc;
   if (T > kMaxTokens || q_heads > 65536 || seqs > 65535 || max_q > kMaxTokens ||
       table_width > (kMaxTokens >> h->kv.page_shift))
@@ -194,19 +207,21 @@ int fc_gguf_kv_attend(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_hea
   a.group = q_heads / h->kv.kv_heads;
   a.max_q = (int)(max_q < T ? max_q : T);
   a.window = window;
-  a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
+  a.scale_log2 = scale_log2;
   // a launch has under 2^32 threads
   if ((int64_t)a.max_q * a.group > kMaxTokens ||
       ((int64_t)a.max_q * a.group / 16 + 1) * seqs * h->kv.kv_heads >= ((int64_t)1 << 23))
     return FC_GGUF_ERANGE;
   const fcg::AttendPlan p = fcg::attend_plan(a, h->num_cu);
-  const size_t need = fcg::attend_workspace_bytes(a, p);
-  if (need) {
-    const int rc = ensure_kv_ws(h, need, (hipStream_t)stream);
-    if (rc != FC_GGUF_OK) return rc;
-    a.part = (float*)h->ws;
-  }
-  return fcg::launch_attend(a, p, h->dtype, (hipStream_t)stream) == hipSuccess ? FC_GGUF_OK : FC_GGUF_EHIP;
+  const int rc = ensure_kv_ws(h, seqs * h->kv.kv_heads, fcg::attend_workspace_bytes(a, p), (hipStream_t)stream);
+  if (rc != FC_GGUF_OK) return rc;
+  a.arrived = (uint32_t*)h->ws;
+  a.counters = h->counters;
+  a.fresh = h->fresh;
+  a.part = (float*)((char*)h->ws + counter_bytes(h->counters));
+  if (fcg::launch_attend(a, p, h->dtype, (hipStream_t)stream) != hipSuccess) return FC_GGUF_EHIP;
+  h->fresh = false;
+  return FC_GGUF_OK;
 }
 
 int fc_gguf_logits(const void* x, int64_t x_stride, int dtype, int64_t rows, int64_t vocab,
