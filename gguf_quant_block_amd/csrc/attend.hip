@@ -54,11 +54,9 @@ struct Piece {
     // The page of the 16 keys that hold a lane's key rows (r / 8) and of those
     // that hold its values (g / 2); a page never ends inside 16 keys.  -1: no
     // page of the pool, its keys take no part.
-    auto page_at = [&](int key) -> int {
-      if (key >= c1) return -1;
-      const int p = table[key >> a.kv.page_shift];
-      return (unsigned)p < (uint64_t)a.kv.pages ? p : -1;
-    };
+    // Entries of the table are read a step before they are looked at.
+    auto entry_at = [&](int key) -> int { return table[(key < c1 ? key : c1 - 1) >> a.kv.page_shift]; };
+    auto page_of = [&](int key, int entry) -> int { return key < c1 && (unsigned)entry < (uint64_t)a.kv.pages ? entry : -1; };
     u32x4 kr[2][KS], vr[DT];
     // key of row r of half h of a tile: 8 (r / 4) + 4 h + r % 4
     auto load_k = [&](int tok0, int page) {
@@ -92,11 +90,17 @@ struct Piece {
 
     const int first = c0 + wave * AT_TILE, ko = (r >> 3) * 16, vo = (g >> 1) * 16;
     int tok0 = first;
-    // pages of the tile and of the next one (its loads do not wait for the table)
-    int pk = page_at(tok0 + ko), pv = page_at(tok0 + vo);
-    int npk = page_at(tok0 + AT_STEP + ko), npv = page_at(tok0 + AT_STEP + vo);
-    load_k(tok0, pk);
-    load_v(tok0, pv);
+    int ek = 0, ev = 0, pv = -1;                   // entries of the next tile, page of this one's values
+    if (tok0 < c1) {
+      ek = entry_at(tok0 + ko);
+      ev = entry_at(tok0 + vo);
+      const int pk = page_of(tok0 + ko, ek);
+      pv = page_of(tok0 + vo, ev);
+      ek = entry_at(tok0 + AT_STEP + ko);
+      ev = entry_at(tok0 + AT_STEP + vo);
+      load_k(tok0, pk);
+      load_v(tok0, pv);
+    }
     u32x4 q[RT][KS];
     int pos[RT];
 #pragma unroll
@@ -128,8 +132,8 @@ struct Piece {
           sc[i][h] = c;
         }
       // (past the last tile the loads are of the pool's first page, for nothing)
-      load_k(next, npk);
-      npk = page_at(next + AT_STEP + ko);
+      load_k(next, page_of(next + ko, ek));
+      ek = entry_at(next + AT_STEP + ko);
 
       if (!is_open(tok0, pv)) {
         const int key0 = tok0 + 8 * g, n = have(tok0, pv);
@@ -176,14 +180,14 @@ struct Piece {
           o[i][d] = Mat<E>::mfma16(vr[d], w, o[i][d]);
         }
       }
-      load_v(next, npv);
-      pv = npv;
-      npv = page_at(next + AT_STEP + vo);
+      pv = page_of(next + vo, ev);
+      load_v(next, pv);
+      ev = entry_at(next + AT_STEP + vo);
     }
 
     if (__any(bad != 0))                           // counts of the values taken out
       for (tok0 = first; tok0 < c1; tok0 += AT_STEP) {
-        const int page = page_at(tok0 + (g >> 1) * 16);
+        const int page = page_of(tok0 + vo, entry_at(tok0 + vo));
         if (is_open(tok0, page)) continue;
         const int key0 = tok0 + 8 * g, n = have(tok0, page);
         const uint8_t* p = v_at(tok0, page);
@@ -470,18 +474,24 @@ __global__ __launch_bounds__(at_waves(D) * 64, at_waves(D) / 4) void attend_stre
     if (last_piece[k]) join_pieces<E, D>(a, piece_q0[k], piece_rows[k], hk, x0[k], x1[k], sums);
 }
 
-// Joins the splits of a row of the tile kernel: a wave per row, D / 64
+// Joins the splits of a row of the tile kernel: a wave per row of q, D / 64
 // dimensions per lane.
 template <class E, int D>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
   constexpr int N = (D + 63) / 64;
   const int lane = threadIdx.x & 63;
-  const int64_t rr = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);   // row of the sequence
-  const int tok = (int)(rr / a.q_heads), head = (int)(rr - (int64_t)tok * a.q_heads);
-  const int hk = head / a.group, row = tok * a.group + head - hk * a.group;
-  RowTile t;
-  if (!row_tile(a, blockIdx.y, hk, row, 1, a.stream_rows + 1, INT32_MAX, 1, t)) return;
-  const int64_t orow = (int64_t)(t.q0 + tok) * a.q_heads + head;
+  const int64_t orow = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), tok = orow / a.q_heads;
+  if (tok >= a.T) return;
+  const int head = (int)(orow - tok * a.q_heads);
+  // the token's sequence, if it is the tile kernel's
+  bool mine = false;
+  for (int s0 = 0; s0 < a.seqs && !mine; s0 += 64) {
+    RowTile t;
+    const int s = s0 + lane;
+    mine = __any(s < a.seqs && row_tile(a, s, 0, 0, 1, a.stream_rows + 1, INT32_MAX, 1, t) && tok >= t.q0 &&
+                 tok < t.q0 + t.rows / a.group);
+  }
+  if (!mine) return;
   const int64_t first = orow, step = a.T * a.q_heads;
   float mt = -INFINITY;
   for (int x = lane; x < a.splits; x += 64) mt = fmaxf(mt, a.part_ml[(first + x * step) * 2]);
@@ -511,7 +521,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
   for (int j = 0; j < N; ++j) {
     const int d = j * 64 + lane;
     if (D % 64 == 0 || d < D)
-      a.o[(t.q0 + tok) * a.o_stride + head * D + d] = __builtin_bit_cast(uint16_t, (E)(y[j] * f));
+      a.o[tok * a.o_stride + head * D + d] = __builtin_bit_cast(uint16_t, (E)(y[j] * f));
   }
   if (a.lse && lane == 0) a.lse[orow] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * LN2;
 }
@@ -519,8 +529,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
 template <class E, int D>
 hipError_t join_launch(const AttendArgs& a, hipStream_t st) {
   if (a.splits == 1) return hipSuccess;
-  const int64_t rows = (int64_t)a.max_q * a.q_heads;     // of a sequence, in the order of q
-  attend_join_kernel<E, D><<<dim3((unsigned)((rows + 3) / 4), (unsigned)a.seqs), 256, 0, st>>>(a);
+  attend_join_kernel<E, D><<<dim3((unsigned)((a.T * a.q_heads + 3) / 4)), 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -588,13 +597,17 @@ AttendPlan attend_plan(const AttendArgs& a, int num_cu) {
   p.whole = span(p.stream_rows, AT_TILE) <= 4 * at_step(D);
   if (p.whole) p.splits = a.seqs;
   if (rows > most) {
-    // tiles of 256 rows where there are enough of them for every CU
+    // where every sequence has max_q rows (if cu_q says so too), all are the tile kernel's
+    if (a.T >= a.max_q * (int64_t)a.seqs) p.stream_rows = 0;
+    // tiles of 256 rows where there are enough of them for every CU (of 96
+    // dimensions the pieces cannot be dealt to 8 waves, and 256 take the
+    // registers of two waves)
     const int64_t all = a.T * a.group;
-    p.tile_rows = D <= 128 && all / 256 * hk >= num_cu ? 256 : 128;
+    p.tile_rows = (D == 64 || D == 128) && all / 256 * hk >= num_cu ? 256 : 128;
     const int64_t tiles = ((all + p.tile_rows - 1) / p.tile_rows) * hk;
     // (the grid has under 2^23 workgroups, those without rows among them)
     const int64_t grid = (rows + p.tile_rows - 1) / p.tile_rows * hk * a.seqs, room = ((int64_t)1 << 23) / grid;
-    int64_t want = tiles < num_cu ? (2 * num_cu + tiles - 1) / tiles : 1;
+    int64_t want = 2 * num_cu / tiles;
     if (want > room) want = room;
     p.tile_splits = split_plan(span(p.tile_rows, 64), want, 512, 64, &p.tile_per);
   }
@@ -632,6 +645,7 @@ hipError_t launch_attend(const AttendArgs& args, const AttendPlan& p, int dtype,
     if (e == hipSuccess) e = dtype == DT_F16 ? launch_e<f16>(a, true, st) : launch_e<bf16>(a, true, st);
     if (e != hipSuccess) return e;
   }
+  if (p.stream_rows == 0) return hipSuccess;
   return dtype == DT_F16 ? launch_e<f16>(a, false, st) : launch_e<bf16>(a, false, st);
 }
 

@@ -2,8 +2,8 @@
 // head): tiles of rows against tiles of 64 keys in LDS.
 //
 // The rows of one key head are the tokens times the group of query heads that
-// share it, token by token; a wave has RB * 32 of them, a workgroup WAVES
-// times as many, and the keys and values of a tile are read once for all.
+// share it, token by token; a wave has 32 of them, a workgroup 32 WAVES, and
+// the keys and values of a tile are read once for all.
 //
 // S^T = K Q^T and O^T = V^T P^T on 32x32x16 matrix instructions: a lane holds
 // scores of one query row (column lane % 32).  Operand row 8a + 4h + b of the
@@ -15,9 +15,11 @@
 // [8][D] of values) whatever the page size, and every LDS read is a
 // contiguous 1024 bytes.
 //
-// The reference point m of a row's exponentials follows its maximum only when
-// that has grown by more than 2^LAZY: the weights stay below 2^LAZY (in range
-// of f16), and most tiles leave the sums as they are.
+// The reference point m of a row's exponentials is a maximum of some earlier
+// tile.  A tile's weights are taken against it as it stands; only if their sum
+// then passes MOST (or m is still -inf) is the tile's maximum looked for, m
+// moved and the weights taken again.  Weights stay below MOST, in range of
+// f16, and most tiles cost no maximum and leave the sums as they are.
 #include <math.h>
 
 #include "attend.h"
@@ -26,11 +28,11 @@ namespace fcg {
 namespace {
 
 constexpr int KT = 64;                           // keys of a tile
-constexpr float LAZY = 8.f;
+constexpr float MOST = 4096.f;
 
-template <int D, int RB, int WAVES>
+template <int D, int WAVES>
 struct TileCfg {
-  static constexpr int ROWS = WAVES * RB * 32;
+  static constexpr int ROWS = WAVES * 32;
   static constexpr int KB = KT * D * 2;          // bytes of a tile's keys, and of its values
   static constexpr int STAGE = 2 * KB;           // values of a tile, then keys of the next
   static constexpr int STAGES = D <= 128 ? 3 : 2;
@@ -48,11 +50,18 @@ __device__ __forceinline__ void half_barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-template <class E, int D, int RB, int WAVES>
-__global__ __launch_bounds__(WAVES * 64, WAVES == 4 && RB == 1 && D <= 128 ? 2 : 1) void attend_tile_kernel(AttendArgs a) {
-  using C = TileCfg<D, RB, WAVES>;
+// half_barrier() of the waves for which `on`, the same in every lane, holds.
+__device__ __forceinline__ void barrier_if(bool on) {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_cmp_eq_u32 %0, 0\n\ts_cbranch_scc1 1f\n\ts_barrier\n1:" ::"s"(__builtin_amdgcn_readfirstlane((int)on)) : "memory", "scc");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+template <class E, int D, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kernel(AttendArgs a) {
+  using C = TileCfg<D, WAVES>;
   static_assert(D / 8 % WAVES == 0, "pieces per wave");
-  constexpr int KS = D / 16, DB = D / 32, NI = C::NI;
+  constexpr int KS = D / 16, DB = D / 32, NI = C::NI, READS = 2 * KS + 4 * DB, AHEAD = 6;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -76,63 +85,57 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 4 && RB == 1 && D <= 128 ? 2 :
   const int32_t* table = a.table + t.s * a.table_stride;
 
   // rows of this wave
-  const int wrow0 = t.row0 + wave * RB * 32;
-  const int wlast = (wrow0 + RB * 32 < t.rows ? wrow0 + RB * 32 : t.rows) - 1;
+  const int wrow0 = t.row0 + wave * 32;
+  const int wlast = (wrow0 + 32 < t.rows ? wrow0 + 32 : t.rows) - 1;
   const bool any_rows = wrow0 < t.rows;
   const int wlo = t.base + wrow0 / a.group, whi = any_rows ? t.base + wlast / a.group : -1;
 
-  u32x4 q[RB][KS];
-  int pos[RB];
+  // this lane's row
+  const int row = wrow0 + r;
+  const bool there = row < t.rows;
+  const int tok = row / a.group, pos = there ? t.base + tok : -1;
+  float m = there ? -INFINITY : 0.f, l = 0.f;    // reference point, total (of the lane half's keys)
+  u32x4 q[KS];
+  const uint16_t* p = a.q + (t.q0 + tok) * a.q_stride + (hk * a.group + row - tok * a.group) * D + h * 8;
 #pragma unroll
-  for (int i = 0; i < RB; ++i) {
-    const int row = wrow0 + i * 32 + r;
-    const bool there = row < t.rows;
-    const int tok = row / a.group;
-    pos[i] = there ? t.base + tok : -1;
-    const uint16_t* p = a.q + (t.q0 + tok) * a.q_stride + (hk * a.group + row - tok * a.group) * D + h * 8;
-#pragma unroll
-    for (int k = 0; k < KS; ++k) q[i][k] = there ? *(const u32x4*)(p + k * 16) : (u32x4){0, 0, 0, 0};
-  }
+  for (int k = 0; k < KS; ++k) q[k] = there ? *(const u32x4*)(p + k * 16) : (u32x4){0, 0, 0, 0};
 
-  floatx16 o[RB][DB];
-  float m[RB], l[RB];
+  floatx16 o[DB];
 #pragma unroll
-  for (int i = 0; i < RB; ++i) {
-    m[i] = -INFINITY;
-    l[i] = 0.f;
+  for (int d = 0; d < DB; ++d)
 #pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-      for (int x = 0; x < 16; ++x) o[i][d][x] = 0.f;
-  }
+    for (int x = 0; x < 16; ++x) o[d][x] = 0.f;
 
-  // page of key tok0 + lane, -1: none of the pool (its keys take no part)
-  auto page_at = [&](int tok0) -> int {
-    const int key = tok0 + lane;
-    if (key >= c1) return -1;
-    const int p = table[key >> a.kv.page_shift];
-    return (unsigned)p < (uint64_t)a.kv.pages ? p : -1;
+  // Key tok0 + lane: its entry in the table (read a tile before it is looked
+  // at, so that nothing waits for it), its page, -1 for none of the pool (its
+  // keys take no part), and where the page begins in bytes.
+  auto entry_at = [&](int tok0) -> int {
+    const int key = tok0 + lane < c1 ? tok0 + lane : c1 - 1;
+    return *(const int32_t*)((const uint8_t*)table + (uint32_t)(key >> a.kv.page_shift) * 4u);
   };
+  auto page_of = [&](int tok0, int entry) -> int {
+    return tok0 + lane < c1 && (unsigned)entry < (uint64_t)a.kv.pages ? entry : -1;
+  };
+  auto start_of = [&](int page) -> uint64_t { return (uint32_t)(page < 0 ? 0 : page) * (uint64_t)(uint32_t)page_bytes; };
   // pieces of keys and of values on their way to LDS
   u32x4 kst[NI], vst[NI];
-  auto load_k = [&](int tok0, int page) {
-    const uint8_t* kp = kbase + (page < 0 ? 0 : page) * page_bytes + ((tok0 + lane) & (ps - 1)) * 16;
+  auto load_k = [&](int tok0, uint64_t start) {
+    const uint8_t* kp = kbase + start + (((tok0 + lane) & (ps - 1)) * 16 + wave * NI * ps * 16);
 #pragma unroll
-    for (int i = 0; i < NI; ++i) kst[i] = *(const u32x4*)(kp + (int64_t)(wave * NI + i) * ps * 16);
+    for (int i = 0; i < NI; ++i) kst[i] = *(const u32x4*)(kp + (uint32_t)(i * ps * 16));
   };
-  auto load_v = [&](int tok0, int page) {
-    page = page < 0 ? 0 : page;
+  auto load_v = [&](int tok0, uint64_t start) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       if constexpr (D % 64 == 0) {               // the wave's 64 pieces are of the same 8 keys
         const int p = (wave * NI + i) * 64, k8 = p / D, d = p - k8 * D;
-        const uint8_t* vp = vbase + __builtin_amdgcn_readlane(page, k8 * 8) * page_bytes +
-                            (((tok0 + k8 * 8) & (ps - 1)) >> 3) * (D * 16) + d * 16;
-        vst[i] = *(const u32x4*)(vp + lane * 16);
+        const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(start >> 32), k8 * 8) << 32 |
+                            (uint32_t)__builtin_amdgcn_readlane((int)start, k8 * 8);
+        const uint8_t* vp = vbase + at + (uint32_t)(((tok0 + k8 * 8) & (ps - 1)) * (D * 2) + d * 16);
+        vst[i] = *(const u32x4*)(vp + (uint32_t)lane * 16);
       } else {
         const int p = (wave * NI + i) * 64 + lane, k8 = p / D, d = p - k8 * D;
-        vst[i] = *(const u32x4*)(vbase + __shfl(page, k8 * 8) * page_bytes + (((tok0 + k8 * 8) & (ps - 1)) >> 3) * (D * 16) +
-                                 d * 16);
+        vst[i] = *(const u32x4*)(vbase + __shfl(start, k8 * 8) + (uint32_t)(((tok0 + k8 * 8) & (ps - 1)) * (D * 2) + d * 16));
       }
     }
   };
@@ -172,22 +175,19 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 4 && RB == 1 && D <= 128 ? 2 :
     if (bad) *flag = 1;
   };
 
-  floatx16 sc[RB][2];                            // scores
-  u32x4 w[RB][4];                                // weights
+  floatx16 sc[2];                            // scores
+  u32x4 w[4];                                // weights
   auto scores = [&](int stage) {
 #pragma unroll
-    for (int i = 0; i < RB; ++i)
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int x = 0; x < 16; ++x) sc[i][n][x] = 0.f;
+      for (int x = 0; x < 16; ++x) sc[n][x] = 0.f;
 #pragma unroll
     for (int k = 0; k < KS; ++k)
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         const u32x4 kk = *(const u32x4*)(kop + stage + k * 2 * KT * 16 + n * 32 * 16);
-#pragma unroll
-        for (int i = 0; i < RB; ++i) sc[i][n] = Mat<E>::mfma32(kk, q[i][k], sc[i][n]);
+        sc[n] = Mat<E>::mfma32(kk, q[k], sc[n]);
       }
   };
   auto weights = [&](int tok0, uint64_t ok) {
@@ -195,48 +195,44 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 4 && RB == 1 && D <= 128 ? 2 :
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         const int key0 = tok0 + s * 16 + 8 * h, n = have(tok0, ok, 2 * s + h);
+        const int top = pos - key0 < n ? pos - key0 : n - 1;       // last key that the row sees
+        const int low = a.window > 0 ? pos - a.window - key0 : -1;    // last before its window
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
-          const int top = pos[i] - key0 < n ? pos[i] - key0 : n - 1;       // last key that the row sees
-          const int low = a.window > 0 ? pos[i] - a.window - key0 : -1;    // last before its window
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j > top || j <= low) sc[i][s >> 1][(s & 1) * 8 + j] = -INFINITY;
-        }
+        for (int j = 0; j < 8; ++j)
+          if (j > top || j <= low) sc[s >> 1][(s & 1) * 8 + j] = -INFINITY;
       }
     }
+    auto take = [&](float ms) -> float {       // weights against the reference point ms, their sum
+      float sum[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < RB; ++i) {
-      float mx = fmaxf(sc[i][0][0], sc[i][1][0]);
+      for (int s = 0; s < 4; ++s)
 #pragma unroll
-      for (int x = 1; x < 16; ++x) mx = max3(mx, sc[i][0][x], sc[i][1][x]);
+        for (int j = 0; j < 4; ++j) {
+          const float x = sc[s >> 1][(s & 1) * 8 + 2 * j], y = sc[s >> 1][(s & 1) * 8 + 2 * j + 1];
+          const float px = __builtin_amdgcn_exp2f(fmaf(x, a.scale_log2, -ms)), py = __builtin_amdgcn_exp2f(fmaf(y, a.scale_log2, -ms));
+          w[s][j] = pack2<E>(px, py);
+          sum[0] += px;
+          sum[1] += py;
+        }
+      return sum[0] + sum[1];
+    };
+    float sum = take(m);
+    if (__any(!(sum <= MOST))) {               // (m = -inf makes it infinite or NaN)
+      float mx = fmaxf(sc[0][0], sc[1][0]);
+#pragma unroll
+      for (int x = 1; x < 16; ++x) mx = max3(mx, sc[0][x], sc[1][x]);
       mx = fmaxf(mx, other_half(mx));
-      const float mn = mx * a.scale_log2;
-      if (__any(mn > m[i] + LAZY)) {             // (also where m is -inf and mn is not)
-        const float to = fmaxf(m[i], mn), ms = to == -INFINITY ? 0.f : to;
-        const float al = __builtin_amdgcn_exp2f(m[i] - ms);
-        m[i] = to;
-        l[i] *= al;
+      const float to = fmaxf(m, mx * a.scale_log2), ms = to == -INFINITY ? 0.f : to;
+      const float al = __builtin_amdgcn_exp2f(m - ms);
+      m = to;
+      l *= al;
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
+      for (int d = 0; d < DB; ++d)
 #pragma unroll
-          for (int x = 0; x < 16; ++x) o[i][d][x] *= al;
-      }
-      const float ms = m[i] == -INFINITY ? 0.f : m[i];
-      float sum = 0.f;
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        float p[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          p[j] = __builtin_amdgcn_exp2f(fmaf(sc[i][s >> 1][(s & 1) * 8 + j], a.scale_log2, -ms));
-          sum += p[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[i][s][j] = pack2<E>(p[2 * j], p[2 * j + 1]);
-      }
-      l[i] += sum;
+        for (int x = 0; x < 16; ++x) o[d][x] *= al;
+      sum = take(ms);
     }
+    l += sum;
   };
   auto values = [&](int stage) {
 #pragma unroll
@@ -244,8 +240,7 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 4 && RB == 1 && D <= 128 ? 2 :
 #pragma unroll
       for (int d = 0; d < DB; ++d) {
         const u32x4 v = *(const u32x4*)(vop + stage + (s * 2 * D + d * 32) * 16);
-#pragma unroll
-        for (int i = 0; i < RB; ++i) o[i][d] = Mat<E>::mfma32(v, w[i][s], o[i][d]);
+        o[d] = Mat<E>::mfma32(v, w[s], o[d]);
       }
   };
 
@@ -253,148 +248,151 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 4 && RB == 1 && D <= 128 ? 2 :
   // Of the loop's two halves one is vector work (weights), one matrix work.
   // With 8 waves, waves 4 to 7 run one half behind waves 0 to 3, their
   // neighbours on the SIMDs, so that one of the two kinds of work is always
-  // next to the other.  Stage n is stored in the first halves of tile n - 2,
-  // read in the second halves of tile n - 1, and free again two halves later.
+  // next to the other.  Stage n is stored in the second halves of tile n - 2 and
+  // read in those of tile n - 1.
   if (c0 < c1) {
-    const bool behind = wave >= 4;
-    const int p0 = page_at(c0), p1 = page_at(c0 + KT);
-    int p2 = page_at(c0 + 2 * KT), p3 = page_at(c0 + 3 * KT);
-    uint64_t ok = __ballot(p0 >= 0), ok1 = __ballot(p1 >= 0), ok2 = __ballot(p2 >= 0);
-    load_k(c0, p0);
+    const int p0 = page_of(c0, entry_at(c0)), p1 = page_of(c0 + KT, entry_at(c0 + KT));
+    const int p2 = page_of(c0 + 2 * KT, entry_at(c0 + 2 * KT));
+    int e3 = entry_at(c0 + 3 * KT);
+    uint64_t ok = __ballot(p0 >= 0), ok1 = __ballot(p1 >= 0), ok2 = __ballot(p2 >= 0), start2 = start_of(p2);
+    load_k(c0, start_of(p0));
     store(C::KB, kst);
-    load_v(c0, p0);
-    load_k(c0 + KT, p1);
+    load_v(c0, start_of(p0));
+    load_k(c0 + KT, start_of(p1));
     clean(c0, ok);
     store(C::STAGE, vst);
     store(C::STAGE + C::KB, kst);
-    load_v(c0 + KT, p1);
-    load_k(c0 + 2 * KT, p2);
+    load_v(c0 + KT, start_of(p1));
+    load_k(c0 + 2 * KT, start2);
     half_barrier();
     scores(0);
-    if (behind || C::STAGES == 2) half_barrier();
+    if constexpr (WAVES > 4) barrier_if(wave >= 4);
+    if constexpr (C::STAGES == 2) half_barrier();
     int cur = C::STAGE, next = C::STAGES == 2 ? 0 : 2 * C::STAGE;
     for (int tok0 = c0; tok0 < c1; tok0 += KT) {
+      const int p3 = page_of(tok0 + 3 * KT, e3);
+      const uint64_t ok3 = __ballot(p3 >= 0), start3 = start_of(p3);
+      weights(tok0, ok);
+      half_barrier();
       // (past the last tile the loads are of keys without a page, never read)
       clean(tok0 + KT, ok1);
       store(next, vst);
       store(next + C::KB, kst);
-      load_v(tok0 + 2 * KT, p2);
-      load_k(tok0 + 3 * KT, p3);
-      p2 = p3;
-      p3 = page_at(tok0 + 4 * KT);
-      weights(tok0, ok);
-      half_barrier();
+      load_v(tok0 + 2 * KT, start2);
+      load_k(tok0 + 3 * KT, start3);
+      e3 = entry_at(tok0 + 4 * KT);
       values(cur);
       scores(cur);
+      // LDS reads run AHEAD operands before the matrix instructions that use
+      // them (left alone, two: every pair then waits for the LDS)
+#pragma unroll
+      for (int x = 0; x < READS + AHEAD; ++x) {
+        if (x >= AHEAD) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (x < READS) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
       half_barrier();
       cur = next;
       next = next + C::STAGE == C::STAGES * C::STAGE ? 0 : next + C::STAGE;
       ok = ok1;
       ok1 = ok2;
-      ok2 = __ballot(p2 >= 0);
+      ok2 = ok3;
+      start2 = start3;
     }
-    if (WAVES > 4 && !behind) half_barrier();
+    if constexpr (WAVES > 4) barrier_if(wave < 4);
   }
 
   if (c0 < c1 && *flag) {                        // (all waves have passed the loop's last barrier)
     for (int tok0 = c0; tok0 < c1; tok0 += KT) {
-      const int page = page_at(tok0);
+      const int page = page_of(tok0, entry_at(tok0));
       const uint64_t ok = __ballot(page >= 0);
       if (is_open(tok0, ok, t.lo, t.hi)) continue;
       const int in_page = tok0 & (ps - 1);
 #pragma unroll
-      for (int d = 0; d < DB; ++d)
+      for (int d = 0; d < DB; ++d) {
+        floatx16 c;
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
-          floatx16 c;
+        for (int x = 0; x < 16; ++x) c[x] = 0.f;
 #pragma unroll
-          for (int x = 0; x < 16; ++x) c[x] = 0.f;
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            const int key0 = tok0 + s * 16 + 8 * h, n = have(tok0, ok, 2 * s + h);
-            const u32x4 one =
-                seen_ones<E>(pos[i] - key0 < n ? pos[i] - key0 : n - 1, a.window > 0 ? pos[i] - a.window - key0 : -1);
-            const int pg = __shfl(page, s * 16 + 8 * h);
-            const u32x4 v = *(const u32x4*)(vbase + (pg < 0 ? 0 : pg) * page_bytes +
-                                            ((((in_page + s * 16 + 8 * h) & (ps - 1)) >> 3) * D + d * 32 + r) * 16);
-            c = Mat<E>::mfma32(nonfinite_codes<E>(v & keep_keys(n)), one, c);
-          }
-#pragma unroll
-          for (int x = 0; x < 16; ++x) o[i][d][x] += nonfinite_sum(c[x]);
+        for (int s = 0; s < 4; ++s) {
+          const int key0 = tok0 + s * 16 + 8 * h, n = have(tok0, ok, 2 * s + h);
+          const u32x4 one = seen_ones<E>(pos - key0 < n ? pos - key0 : n - 1, a.window > 0 ? pos - a.window - key0 : -1);
+          const int pg = __shfl(page, s * 16 + 8 * h);
+          const u32x4 v = *(const u32x4*)(vbase + start_of(pg) +
+                                          ((((in_page + s * 16 + 8 * h) & (ps - 1)) >> 3) * D + d * 32 + r) * 16);
+          c = Mat<E>::mfma32(nonfinite_codes<E>(v & keep_keys(n)), one, c);
         }
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[d][x] += nonfinite_sum(c[x]);
+      }
     }
   }
 
-  // rows out: through LDS, a wave's 32 rows at a time (the loop's last barrier
-  // has passed: no wave reads the tiles any more)
+  const float lt = l + __shfl_xor(l, 32);
+  const int head = hk * a.group + row - tok * a.group;
+  const int64_t orow = (int64_t)(t.q0 + tok) * a.q_heads + head;
+  if (a.splits > 1) {
+    if (there) {
+      const int64_t at = (int64_t)split * a.T * a.q_heads + orow;
+      if (h == 0) *(float2*)(a.part_ml + at * 2) = make_float2(m, lt);
+      if (c0 < c1) {
+        float* p = a.part + at * D + 4 * h;
 #pragma unroll
-  for (int i = 0; i < RB; ++i) {
-    const float lt = l[i] + __shfl_xor(l[i], 32);
-    const int row = wrow0 + i * 32 + r;
-    const int tok = row / a.group, head = hk * a.group + row - tok * a.group;
-    const int64_t orow = (int64_t)(t.q0 + tok) * a.q_heads + head;
-    if (a.splits > 1) {
-      if (row < t.rows) {
-        const int64_t at = (int64_t)split * a.T * a.q_heads + orow;
-        if (h == 0) *(float2*)(a.part_ml + at * 2) = make_float2(m[i], lt);
-        if (c0 < c1) {
-          float* p = a.part + at * D + 4 * h;
+        for (int d = 0; d < DB; ++d)
 #pragma unroll
-          for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              *(floatx4*)(p + d * 32 + 8 * x) =
-                  (floatx4){o[i][d][4 * x], o[i][d][4 * x + 1], o[i][d][4 * x + 2], o[i][d][4 * x + 3]};
-        }
-      }
-      continue;
-    }
-    const float f = lt == 0.f ? 0.f : 1.f / lt;
-    // 16-byte chunk c of row r at place c ^ (r & SWZ) of the row, for the banks
-    constexpr int SWZ = D == 96 ? 3 : 7;
-    static_assert(WAVES * 32 * D * 2 <= C::STAGES * C::STAGE, "rows fit");
-    uint8_t* s = smem + wave * 32 * D * 2;
-#pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        uint2 z;
-        z.x = pack2<E>(o[i][d][4 * x] * f, o[i][d][4 * x + 1] * f);
-        z.y = pack2<E>(o[i][d][4 * x + 2] * f, o[i][d][4 * x + 3] * f);
-        *(uint2*)(s + r * (D * 2) + ((d * 4 + x) ^ (r & SWZ)) * 16 + h * 8) = z;
-      }
-    if (a.lse && h == 0 && row < t.rows) a.lse[orow] = lt == 0.f ? -INFINITY : (m[i] + log2f(lt)) * LN2;
-    // (within a wave: LDS operations complete in order)
-    __builtin_amdgcn_wave_barrier();
-    for (int x = lane; x < 32 * (D / 8); x += 64) {
-      const int rr = x / (D / 8), c = x - rr * (D / 8), row2 = wrow0 + i * 32 + rr;
-      if (row2 < t.rows) {
-        const int tok2 = row2 / a.group, head2 = hk * a.group + row2 - tok2 * a.group;
-        *(u32x4*)(a.o + (t.q0 + tok2) * a.o_stride + head2 * D + c * 8) =
-            *(const u32x4*)(s + rr * (D * 2) + (c ^ (rr & SWZ)) * 16);
+          for (int x = 0; x < 4; ++x)
+            *(floatx4*)(p + d * 32 + 8 * x) =
+                (floatx4){o[d][4 * x], o[d][4 * x + 1], o[d][4 * x + 2], o[d][4 * x + 3]};
       }
     }
-    __builtin_amdgcn_wave_barrier();
+    return;
+  }
+  // rows out: through LDS (the loop's last barrier has passed: no wave reads
+  // the tiles any more)
+  const float f = lt == 0.f ? 0.f : 1.f / lt;
+  // 16-byte chunk c of row r at place c ^ (r & SWZ) of the row, for the banks
+  constexpr int SWZ = D == 96 ? 3 : 7;
+  static_assert(WAVES * 32 * D * 2 <= C::STAGES * C::STAGE, "rows fit");
+  uint8_t* s = smem + wave * 32 * D * 2;
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      uint2 z;
+      z.x = pack2<E>(o[d][4 * x] * f, o[d][4 * x + 1] * f);
+      z.y = pack2<E>(o[d][4 * x + 2] * f, o[d][4 * x + 3] * f);
+      *(uint2*)(s + r * (D * 2) + ((d * 4 + x) ^ (r & SWZ)) * 16 + h * 8) = z;
+    }
+  if (a.lse && h == 0 && there) a.lse[orow] = lt == 0.f ? -INFINITY : (m + log2f(lt)) * LN2;
+  // (within a wave: LDS operations complete in order)
+  __builtin_amdgcn_wave_barrier();
+  for (int x = lane; x < 32 * (D / 8); x += 64) {
+    const int rr = x / (D / 8), c = x - rr * (D / 8), row2 = wrow0 + rr;
+    if (row2 < t.rows) {
+      const int tok2 = row2 / a.group, head2 = hk * a.group + row2 - tok2 * a.group;
+      *(u32x4*)(a.o + (t.q0 + tok2) * a.o_stride + head2 * D + c * 8) =
+          *(const u32x4*)(s + rr * (D * 2) + (c ^ (rr & SWZ)) * 16);
+    }
   }
 }
 
-template <class E, int D, int RB, int WAVES>
+template <class E, int D, int WAVES>
 hipError_t tile_launch(const AttendArgs& args, hipStream_t st) {
-  using C = TileCfg<D, RB, WAVES>;
+  using C = TileCfg<D, WAVES>;
   static std::atomic<uint64_t> raised{0};
-  const hipError_t e = raise_lds_limit((const void*)attend_tile_kernel<E, D, RB, WAVES>, C::LDS, raised);
+  const hipError_t e = raise_lds_limit((const void*)attend_tile_kernel<E, D, WAVES>, C::LDS, raised);
   if (e != hipSuccess) return e;
   AttendArgs a = args;
   a.tiles = (int)(((int64_t)a.max_q * a.group + C::ROWS - 1) / C::ROWS);
   const int64_t wgs = (int64_t)a.tiles * a.seqs * a.splits * a.kv.kv_heads;
-  attend_tile_kernel<E, D, RB, WAVES><<<dim3((unsigned)wgs), WAVES * 64, C::LDS, st>>>(a);
+  attend_tile_kernel<E, D, WAVES><<<dim3((unsigned)wgs), WAVES * 64, C::LDS, st>>>(a);
   return hipGetLastError();
 }
 
 template <class E, int D>
 hipError_t tile_d(const AttendArgs& a, const AttendPlan& p, hipStream_t st) {
-  if constexpr (D == 256) return tile_launch<E, D, 1, 4>(a, st);
-  else return p.tile_rows == 256 ? tile_launch<E, D, D == 64 ? 2 : 1, D == 64 ? 4 : D == 96 ? 4 : 8>(a, st) : tile_launch<E, D, 1, 4>(a, st);
+  if constexpr (D == 64 || D == 128)
+    if (p.tile_rows == 256) return tile_launch<E, D, 8>(a, st);
+  return tile_launch<E, D, 4>(a, st);
 }
 
 template <class E>
