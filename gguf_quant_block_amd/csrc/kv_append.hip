@@ -24,7 +24,6 @@
 namespace fcg {
 namespace {
 
-constexpr int AP_THREADS = 256;
 constexpr int AP_MAX_TOKENS = 8;
 constexpr int AP_MAX_HALF = 128;     // rotated pairs of a head
 
@@ -53,17 +52,46 @@ __device__ __forceinline__ void rotate8(u32x4& a, u32x4& b, const float2* cs, bo
   }
 }
 
-template <class E>
+// A unit of 16 elements of a head: where it comes from and where it goes.
+struct Unit {
+  int t, h, u;         // token of the workgroup, head (queries, then keys), unit of the head
+  int p0, p1;          // its two pieces: 8 pairs (halves or neighbours), or 16 elements that pass
+};
+
+template <class E, int D, int AP_THREADS>
 __global__ __launch_bounds__(AP_THREADS) void kv_append_kernel(AppendArgs a) {
   __shared__ float2 cs[AP_MAX_TOKENS * AP_MAX_HALF];
   __shared__ int slot[AP_MAX_TOKENS + 8];      // [i + 1]: token i of the workgroup
   __shared__ int run_at[AP_MAX_TOKENS], run_len[AP_MAX_TOKENS], runs;
   const int tid = threadIdx.x;
-  const int D = a.kv.head_dim, ps = 1 << a.kv.page_shift;
+  constexpr int units = D / 16, pieces = D / 8;
+  const int ps = 1 << a.kv.page_shift;
   const int64_t t0 = (int64_t)blockIdx.x * a.tokens_per_wg;
   const int nt = (int)(a.T - t0 < a.tokens_per_wg ? a.T - t0 : a.tokens_per_wg);
-  const int half = a.inv_freq ? a.rot / 2 : 0;
+  const int half = a.inv_freq ? a.rot / 2 : 0, rot_units = half / 8;
   const int64_t top = a.kv.pages << a.kv.page_shift;
+  const int per_token = (a.q_heads + a.kv.kv_heads) * units, all = nt * per_token;
+  const int64_t page_elems = (int64_t)a.kv.kv_heads * ps * D;
+  const int first = blockIdx.y * AP_THREADS + tid, step = a.y_splits * AP_THREADS;
+
+  // the thread's next unit, requested ahead of its use
+  u32x4 x0, x1;
+  Unit w;
+  int t_next = first / per_token, rest = first - t_next * per_token;
+  auto request = [&]() {
+    w.t = t_next;
+    w.h = rest / units;
+    w.u = rest - w.h * units;
+    const bool apart = w.u < rot_units && !a.interleaved;
+    w.p0 = apart ? w.u : 2 * w.u;
+    w.p1 = apart ? w.u + rot_units : 2 * w.u + 1;
+    const uint16_t* src = w.h < a.q_heads ? a.q + (t0 + w.t) * a.q_stride + w.h * D
+                                          : a.k + (t0 + w.t) * a.k_stride + (w.h - a.q_heads) * D;
+    x0 = *(const u32x4*)(src + w.p0 * 8);
+    x1 = *(const u32x4*)(src + w.p1 * 8);
+    for (rest += step; rest >= per_token; rest -= per_token) ++t_next;
+  };
+  if (first < all) request();
 
   // the slots of the tokens, of the one before and of 7 after (-1 where a slot
   // names no place in the cache): a run of V may reach that far
@@ -82,102 +110,120 @@ __global__ __launch_bounds__(AP_THREADS) void kv_append_kernel(AppendArgs a) {
     cs[i] = make_float2(c * a.rope_scale, s * a.rope_scale);
   }
   __syncthreads();
-  if (tid == 0) {
-    int n = 0;
-    for (int i = 0; i < nt; ++i) {
-      const int s = slot[i + 1];
-      // does a run begin with token i?
-      if (s < 0 || ((s & 7) != 0 && slot[i] >= 0 && slot[i] == s - 1)) continue;
-      int len = 1;
-      while (((s + len) & 7) != 0 && slot[i + 1 + len] == s + len) ++len;
-      run_at[n] = i;
-      run_len[n++] = len;
+  if (tid < 64) {                              // the runs of V, a lane for each token
+    bool begins = false;
+    int len = 1;
+    if (tid < nt) {
+      const int s = slot[tid + 1], before = slot[tid];
+      begins = s >= 0 && ((s & 7) == 0 || before < 0 || before != s - 1);
+      bool on = true;
+#pragma unroll
+      for (int k = 1; k < 8; ++k) {
+        on = on && ((s + k) & 7) != 0 && slot[tid + 1 + k] == s + k;
+        len += on;
+      }
     }
-    runs = n;
+    const uint64_t m = __ballot(begins);
+    if (begins) {
+      const int at = __builtin_popcountll(m & (((uint64_t)1 << tid) - 1));
+      run_at[at] = tid;
+      run_len[at] = len;
+    }
+    if (tid == 0) runs = __builtin_popcountll(m);
   }
   __syncthreads();
 
-  const int units = D / 16, heads = a.q_heads + a.kv.kv_heads;
-  const int per_token = heads * units;
-  const int64_t page_elems = (int64_t)a.kv.kv_heads * ps * D;
-  const int rot_units = half / 8;
-  const int first = blockIdx.y * AP_THREADS + tid, step = a.y_splits * AP_THREADS;
-  for (int i = first; i < nt * per_token; i += step) {
-    const int t = i / per_token, rest = i - t * per_token;
-    const int h = rest / units, u = rest - h * units;
-    const bool is_q = h < a.q_heads;
-    const int s = slot[t + 1];
-    if (!is_q && s < 0) continue;
-    // the unit's two pieces: 8 pairs (halves or neighbours), or 16 elements that pass
-    const int p0 = u < rot_units && !a.interleaved ? u : 2 * u;
-    const int p1 = u < rot_units && !a.interleaved ? u + rot_units : 2 * u + 1;
-    const uint16_t* src = is_q ? a.q + (t0 + t) * a.q_stride + h * D
-                               : a.k + (t0 + t) * a.k_stride + (h - a.q_heads) * D;
-    u32x4 x0 = *(const u32x4*)(src + p0 * 8), x1 = *(const u32x4*)(src + p1 * 8);
-    if (u < rot_units) rotate8<E>(x0, x1, cs + t * half + u * 8, a.interleaved);
-    if (is_q) {
-      uint16_t* dst = a.q_out + (t0 + t) * a.o_stride + h * D;
-      *(u32x4*)(dst + p0 * 8) = x0;
-      *(u32x4*)(dst + p1 * 8) = x1;
-    } else {
+  // the first run of V, requested ahead of the units' stores
+  const int per_run = a.kv.kv_heads * pieces, vall = runs * per_run;
+  u32x4 v[8];
+  auto request_v = [&](int i) {
+    const int r = i / per_run, rest = i - r * per_run, h = rest / pieces, d0 = (rest - h * pieces) * 8;
+    const uint16_t* src = a.v + (t0 + run_at[r]) * a.v_stride + h * D + d0;
+    const int len = run_len[r];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < len) v[j] = *(const u32x4*)(src + j * a.v_stride);
+  };
+  if (first < vall) request_v(first);
+
+  for (int i = first; i < all; i += step) {
+    const Unit z = w;
+    u32x4 y0 = x0, y1 = x1;
+    if (i + step < all) request();
+    const int s = slot[z.t + 1];
+    if (z.u < rot_units) rotate8<E>(y0, y1, cs + z.t * half + z.u * 8, a.interleaved);
+    if (z.h < a.q_heads) {
+      uint16_t* dst = a.q_out + (t0 + z.t) * a.o_stride + z.h * D;
+      *(u32x4*)(dst + z.p0 * 8) = y0;
+      *(u32x4*)(dst + z.p1 * 8) = y1;
+    } else if (s >= 0) {
       uint16_t* dst = (uint16_t*)a.kv.k + (int64_t)(s >> a.kv.page_shift) * page_elems +
-                      (int64_t)(h - a.q_heads) * ps * D + (s & (ps - 1)) * 8;
-      *(u32x4*)(dst + (int64_t)p0 * ps * 8) = x0;
-      *(u32x4*)(dst + (int64_t)p1 * ps * 8) = x1;
+                      (int64_t)(z.h - a.q_heads) * ps * D + (s & (ps - 1)) * 8;
+      *(u32x4*)(dst + (int64_t)z.p0 * ps * 8) = y0;
+      *(u32x4*)(dst + (int64_t)z.p1 * ps * 8) = y1;
     }
   }
 
-  const int pieces = D / 8, per_run = a.kv.kv_heads * pieces;
-  for (int i = first; i < runs * per_run; i += step) {
-    const int r = i / per_run, rest = i - r * per_run;
-    const int h = rest / pieces, d0 = (rest - h * pieces) * 8;
-    const int t = run_at[r], len = run_len[r], s = slot[t + 1];
-    const uint16_t* src = a.v + (t0 + t) * a.v_stride + h * D + d0;
-    uint16_t* dst = (uint16_t*)a.kv.v + (int64_t)(s >> a.kv.page_shift) * page_elems +
-                    (int64_t)h * ps * D + (int64_t)(((s & (ps - 1)) >> 3) * D + d0) * 8;
+  for (int i = first; i < vall; i += step) {
+    if (i != first) request_v(i);
+    const int r = i / per_run, rest = i - r * per_run, h = rest / pieces, d0 = (rest - h * pieces) * 8;
+    const int len = run_len[r], s = slot[run_at[r] + 1];
+    uint16_t* dst = (uint16_t*)a.kv.v + (int64_t)(s >> a.kv.page_shift) * page_elems + (int64_t)h * ps * D +
+                    (int64_t)(((s & (ps - 1)) >> 3) * D + d0) * 8;
     if (len == 8) {
-      u32x4 x[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = *(const u32x4*)(src + j * a.v_stride);
 #pragma unroll
       for (int d = 0; d < 8; ++d) {
         u32x4 y;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t lo = x[2 * j][d / 2], hi = x[2 * j + 1][d / 2];
+          const uint32_t lo = v[2 * j][d / 2], hi = v[2 * j + 1][d / 2];
           y[j] = d & 1 ? (lo >> 16) | (hi & 0xFFFF0000u) : (lo & 0xFFFFu) | (hi << 16);
         }
         *(u32x4*)(dst + d * 8) = y;
       }
     } else {
-      for (int j = 0; j < len; ++j) {
-        const u32x4 x = *(const u32x4*)(src + j * a.v_stride);
 #pragma unroll
-        for (int d = 0; d < 8; ++d)
-          dst[d * 8 + (s & 7) + j] = (uint16_t)(d & 1 ? x[d / 2] >> 16 : x[d / 2]);
-      }
+      for (int j = 0; j < 8; ++j)
+        if (j < len)
+#pragma unroll
+          for (int d = 0; d < 8; ++d)
+            dst[d * 8 + (s & 7) + j] = (uint16_t)(d & 1 ? v[j][d / 2] >> 16 : v[j][d / 2]);
     }
   }
+}
+
+template <class E, int THREADS>
+hipError_t append_e(const AppendArgs& a, dim3 grid, hipStream_t st) {
+  switch (a.kv.head_dim) {
+    case 64: kv_append_kernel<E, 64, THREADS><<<grid, THREADS, 0, st>>>(a); break;
+    case 96: kv_append_kernel<E, 96, THREADS><<<grid, THREADS, 0, st>>>(a); break;
+    case 128: kv_append_kernel<E, 128, THREADS><<<grid, THREADS, 0, st>>>(a); break;
+    default: kv_append_kernel<E, 256, THREADS><<<grid, THREADS, 0, st>>>(a);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_kv_append(const AppendArgs& args, int dtype, int num_cu, hipStream_t st) {
   AppendArgs a = args;
-  // tokens per workgroup: as many as leave two workgroups per CU
+  // Tokens per workgroup: as many as leave a workgroup per CU.  Where that is
+  // all 8, workgroups of 512 threads (2500 tokens, 40 heads of 128: 17.1 us,
+  // 20.0 with 256 threads and 18.6 with 4 tokens); else of 256 (one token, 96
+  // heads of 96: 4.9 us, 5.6 with 512).
   int tb = AP_MAX_TOKENS;
-  while (tb > 1 && (a.T + tb - 1) / tb < 2 * num_cu) tb /= 2;
+  while (tb > 1 && (a.T + tb - 1) / tb < num_cu) tb /= 2;
+  const int threads = tb == AP_MAX_TOKENS ? 512 : 256;
   a.tokens_per_wg = tb;
   const int64_t wgs = (a.T + tb - 1) / tb;
   // a token's heads over several workgroups, one unit of 16 elements per thread, while CUs are idle
-  const int64_t most = ((int64_t)tb * (a.q_heads + a.kv.kv_heads) * (a.kv.head_dim / 16) + AP_THREADS - 1) / AP_THREADS;
+  const int64_t most = ((int64_t)tb * (a.q_heads + a.kv.kv_heads) * (a.kv.head_dim / 16) + threads - 1) / threads;
   int64_t y = num_cu / wgs;
   y = y < 1 ? 1 : (y > most ? most : y);
   a.y_splits = (int)y;
   const dim3 grid((unsigned)wgs, (unsigned)y);
-  if (dtype == DT_F16) kv_append_kernel<f16><<<grid, AP_THREADS, 0, st>>>(a);
-  else kv_append_kernel<bf16><<<grid, AP_THREADS, 0, st>>>(a);
-  return hipGetLastError();
+  if (threads == 512) return dtype == DT_F16 ? append_e<f16, 512>(a, grid, st) : append_e<bf16, 512>(a, grid, st);
+  return dtype == DT_F16 ? append_e<f16, 256>(a, grid, st) : append_e<bf16, 256>(a, grid, st);
 }
 
 }  // namespace fcg

@@ -8,6 +8,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <atomic>
 #include <new>
 
 #include "fc_gguf.h"
@@ -34,6 +35,17 @@ bool on(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 bool fail_workspace() {
   const char* p = getenv("FC_GGUF_TEST_FAIL_ALLOC");
   return p && (!strcmp(p, "all") || !strcmp(p, "workspace"));
+}
+
+// CUs of the current device, asked for once per device (0: an error)
+int cus_of_current() {
+  static std::atomic<int> known[64];
+  int dev = -1, n = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0) return 0;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 int check_kv_device(const fc_gguf_kv* h) {
@@ -134,7 +146,9 @@ int fc_gguf_kv_append(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_hea
   if (!h || T < 0 || q_heads < 0) return FC_GGUF_EINVAL;
   if (const int rc = check_kv_device(h); rc != FC_GGUF_OK) return rc;
   const int D = h->kv.head_dim, hk = h->kv.kv_heads;
-  if (q_heads > 65536 || T > kMaxTokens) return FC_GGUF_ERANGE;
+  // (a launch has under 2^32 threads)
+  // (a launch has under 2^32 threads: 512 for 8 tokens)
+  if (q_heads > 65536 || T > ((int64_t)1 << 25)) return FC_GGUF_ERANGE;
   if (inv_freq) {
     if (rot_dim <= 0 || rot_dim > D || rot_dim % 16 || axes < 1 || (interleaved != 0 && interleaved != 1) ||
         !on(inv_freq, 4) || (pair_axis && !on(pair_axis, 4)))
@@ -249,10 +263,8 @@ int fc_gguf_logits(const void* x, int64_t x_stride, int dtype, int64_t rows, int
   if (mask && (!on(mask, 4) || mask_stride < (vocab + 31) / 32)) return FC_GGUF_EINVAL;
   if ((repetition && !on(repetition, 4)) || (frequency && !on(frequency, 4)) || (presence && !on(presence, 4)))
     return FC_GGUF_EINVAL;
-  int dev = 0, num_cu = 0;
-  if (hipGetDevice(&dev) != hipSuccess ||
-      hipDeviceGetAttribute(&num_cu, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
-    return FC_GGUF_EHIP;
+  const int num_cu = cus_of_current();
+  if (num_cu <= 0) return FC_GGUF_EHIP;
   fcg::LogitsArgs a = {};
   a.x = x;
   a.out = out;

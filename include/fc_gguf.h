@@ -333,7 +333,7 @@ int fc_gguf_kv_destroy(fc_gguf_kv_t h);
  *              rope_scale multiplies sine and cosine.
  *   q_out      device [T][q_heads][head_dim]; may be q itself with q's stride.
  *              q_heads = 0: keys and values only (q and q_out are not read).
- * q_out must not overlap k or v.  T == 0 is a no-op.  T <= 2^30.
+ * q_out must not overlap k or v.  T == 0 is a no-op.  T <= 2^25.
  */
 int fc_gguf_kv_append(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_heads, const void* k,
                       int64_t k_stride, const void* v, int64_t v_stride, int64_t T, const int32_t* slots,
@@ -366,7 +366,7 @@ int fc_gguf_kv_append(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_hea
  * over workgroups by max_q and table_width, which the host knows; lengths are
  * read on the device, so a captured graph may be replayed with other lengths
  * within them.  The order of summation depends on sizes only.  seqs <= 65535;
- * table_width * page_size <= 2^30; T, seqs or max_q == 0 is a no-op.
+ * table_width * page_size and window <= 2^30; T, seqs or max_q == 0 is a no-op.
  */
 int fc_gguf_kv_attend(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_heads, int64_t T,
                       const int32_t* cu_q, const int32_t* kv_lens, int64_t seqs, const int32_t* table,
