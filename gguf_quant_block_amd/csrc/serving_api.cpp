@@ -58,9 +58,12 @@ size_t counter_bytes(int64_t counters) { return ((size_t)counters * 4 + 255) / 2
 
 // Grows the workspace (counters, then `bytes`) on the call's stream: released
 // to and taken from the device's stream-ordered pool, so that the growth waits
-// for that stream only.
+// for that stream only.  Not while the stream is captured: the memory would
+// belong to the graph.
 int ensure_kv_ws(fc_gguf_kv* h, int64_t counters, size_t bytes, hipStream_t st) {
   if (counters <= h->counters && counter_bytes(h->counters) + bytes <= h->ws_bytes) return FC_GGUF_OK;
+  hipStreamCaptureStatus captured = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(st, &captured) == hipSuccess && captured != hipStreamCaptureStatusNone) return FC_GGUF_ENOMEM;
   if (fail_workspace()) return FC_GGUF_ENOMEM;
   if (counters < h->counters) counters = h->counters;
   if (counters < 1024) counters = 1024;

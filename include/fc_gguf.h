@@ -299,10 +299,10 @@ typedef struct fc_gguf_kv* fc_gguf_kv_t;
  * of one dimension for values.  page_size: a power of two from 16 to 256.
  * head_dim: 64, 96, 128 or 256 (else EUNSUPPORTED).  pages < 2^31,
  * kv_heads <= 1024.  The memory need not be initialised.  The handle belongs
- * to the device current now.  It owns a workspace for attention that is split
- * over the keys, grown stream-ordered as an FC handle's is: one handle must
- * not attend on two streams at once, and a graph is captured after a call of
- * the largest sizes.
+ * to the device current now.  It owns a workspace for attention whose keys are
+ * dealt to several workgroups, grown stream-ordered as an FC handle's is: one
+ * handle must not attend on two streams at once, and a graph is captured after
+ * a call of the largest sizes (growth in a captured stream is FC_GGUF_ENOMEM).
  */
 int fc_gguf_kv_create(int64_t pages, int page_size, int kv_heads, int head_dim, int dtype, void* k_pages,
                       void* v_pages, fc_gguf_kv_t* out);
@@ -362,10 +362,11 @@ int fc_gguf_kv_append(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_hea
  *   lse          device f32[T][q_heads] or NULL: the natural logarithm of the
  *                sum of the exponentials, for joining with other keys
  * A row that sees no key gets zeros and lse -inf; what masked keys and values
- * hold (infinities and NaN included) changes nothing.  The keys are split
- * over workgroups by max_q and table_width, which the host knows; lengths are
- * read on the device, so a captured graph may be replayed with other lengths
- * within them.  The order of summation depends on sizes only.  seqs <= 65535;
+ * hold (infinities and NaN included) changes nothing.  The launches are sized
+ * by T, max_q and table_width, which the host knows; lengths are read on the
+ * device, so a captured graph may be replayed with other lengths within them.
+ * The order of summation depends on sizes and lengths only: equal calls give
+ * equal bits.  seqs <= 65535;
  * table_width * page_size and window <= 2^30; T, seqs or max_q == 0 is a no-op.
  */
 int fc_gguf_kv_attend(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_heads, int64_t T,
