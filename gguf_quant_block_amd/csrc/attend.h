@@ -44,6 +44,35 @@ __device__ __forceinline__ bool row_tile(const AttendArgs& a, int s, int hk, int
   return true;
 }
 
+// The tiles of tile_rows rows of all of the tile kernel's sequences, one after
+// the other: the b-th.  Every wave finds it for itself, 64 sequences at a time.
+// (A grid of max_q for each sequence would be mostly of workgroups without
+// rows: 12 sequences of 1 .. 1031 tokens, 10 us more.)  false: there is none.
+__device__ __forceinline__ bool find_tile(const AttendArgs& a, int b, int hk, int tile_rows, int align, RowTile& t) {
+  const int lane = threadIdx.x & 63;
+  int s = -1, tile = 0;
+  for (int s0 = 0; s0 < a.seqs && s < 0; s0 += 64) {
+    RowTile u;                                     // (of this lane's sequence; t is the same in every lane)
+    const bool rows = s0 + lane < a.seqs && row_tile(a, s0 + lane, hk, 0, 1, a.stream_rows + 1, INT32_MAX, 1, u);
+    const int n = rows ? (u.rows + tile_rows - 1) / tile_rows : 0;
+    int sum = n;
+#pragma unroll
+    for (int k = 1; k < 64; k *= 2) {
+      const int up = __shfl_up(sum, k);
+      if (lane >= k) sum += up;
+    }
+    const uint64_t past = __ballot(sum > b);
+    if (past) {
+      const int i = __builtin_ctzll(past);
+      s = s0 + i;
+      tile = __builtin_amdgcn_readlane(sum, i) - 1 - b;   // the last rows see the most keys: they come first
+    } else {
+      b -= __builtin_amdgcn_readlane(sum, 63);
+    }
+  }
+  return s >= 0 && row_tile(a, s, hk, tile, tile_rows, a.stream_rows + 1, INT32_MAX, align, t);
+}
+
 // keys [c0, c1) of the tile's [beg, end) that split `split` takes: `per` of
 // them each, so that the splits of all sequences cost the same
 __device__ __forceinline__ void split_range(const RowTile& t, int split, int splits, int per, int& c0, int& c1) {
@@ -130,6 +159,12 @@ __device__ __forceinline__ float other_half(float x) {
   asm("" : "+v"(b));                            // (of two equal operands the compiler takes the results for equal too)
   const auto y = __builtin_amdgcn_permlane32_swap(a, b, false, false);   // {own low half twice, own high half twice}
   return __builtin_bit_cast(float, threadIdx.x & 32 ? y[0] : y[1]);
+}
+
+// most tiles of `rows` rows that the sequences of a key head have
+inline int64_t tile_count(const AttendArgs& a, int rows) {
+  const int64_t by_rows = a.T * a.group / rows + a.seqs, each = ((int64_t)a.max_q * a.group + rows - 1) / rows * a.seqs;
+  return by_rows < each ? by_rows : each;
 }
 
 hipError_t launch_attend_tile(const AttendArgs& a, const AttendPlan& p, int dtype, hipStream_t st);

@@ -474,62 +474,56 @@ __global__ __launch_bounds__(at_waves(D) * 64, at_waves(D) / 4) void attend_stre
     if (last_piece[k]) join_pieces<E, D>(a, piece_q0[k], piece_rows[k], hk, x0[k], x1[k], sums);
 }
 
-// Joins the splits of a row of the tile kernel: a wave per row of q, D / 64
-// dimensions per lane.
+// Joins the splits of the tile kernel: four columns of a row are a thread's,
+// in one pass with a running maximum.
+constexpr int join_rows(int D) { return 1024 / D; }   // of a workgroup
 template <class E, int D>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
-  constexpr int N = (D + 63) / 64;
-  const int lane = threadIdx.x & 63;
-  const int64_t orow = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), tok = orow / a.q_heads;
-  if (tok >= a.T) return;
-  const int head = (int)(orow - tok * a.q_heads);
-  // the token's sequence, if it is the tile kernel's
-  bool mine = false;
-  for (int s0 = 0; s0 < a.seqs && !mine; s0 += 64) {
-    RowTile t;
-    const int s = s0 + lane;
-    mine = __any(s < a.seqs && row_tile(a, s, 0, 0, 1, a.stream_rows + 1, INT32_MAX, 1, t) && tok >= t.q0 &&
-                 tok < t.q0 + t.rows / a.group);
-  }
-  if (!mine) return;
-  const int64_t first = orow, step = a.T * a.q_heads;
-  float mt = -INFINITY;
-  for (int x = lane; x < a.splits; x += 64) mt = fmaxf(mt, a.part_ml[(first + x * step) * 2]);
+  constexpr int C4 = D / 4, AHEAD = 4, JOIN_ROWS = join_rows(D);
+  const int hk = blockIdx.x % a.kv.kv_heads;
+  RowTile t;
+  if (!find_tile(a, blockIdx.x / a.kv.kv_heads, hk, JOIN_ROWS, 1, t)) return;
+  const int64_t step = a.T * a.q_heads;                      // rows of a split
+  const int i = threadIdx.x, row = t.row0 + i / C4, d = i % C4 * 4;
+  if (i >= JOIN_ROWS * C4 || row >= t.rows) return;
+  const int tok = row / a.group, head = hk * a.group + row - tok * a.group;
+  const int64_t orow = (int64_t)(t.q0 + tok) * a.q_heads + head;
+  floatx4 y = {0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, l = 0.f;
+  for (int x0 = 0; x0 < a.splits; x0 += AHEAD) {
+    floatx4 z[AHEAD];
+    float2 v[AHEAD];
+    float to = m;
 #pragma unroll
-  for (int k = 1; k < 64; k *= 2) mt = fmaxf(mt, __shfl_xor(mt, k));
-  const float ms = mt == -INFINITY ? 0.f : mt;
-  float lt = 0.f, y[N];
+    for (int k = 0; k < AHEAD; ++k) {
+      const int64_t at = orow + (x0 + k < a.splits ? x0 + k : x0) * step;
+      v[k] = *(const float2*)(a.part_ml + at * 2);
+      z[k] = *(const floatx4*)(a.part + at * D + d);
+    }
 #pragma unroll
-  for (int j = 0; j < N; ++j) y[j] = 0.f;
-  for (int x = 0; x < a.splits; ++x) {
-    const float2 v = *(const float2*)(a.part_ml + (first + x * step) * 2);
-    const bool none = v.x == -INFINITY && v.y == 0.f;        // no keys: its sums are not written
-    const float f = none ? 0.f : __builtin_amdgcn_exp2f(v.x - ms);
-    lt += v.y * f;
-    const float* p = a.part + (first + x * step) * D;
+    for (int k = 0; k < AHEAD; ++k) to = fmaxf(to, v[k].x);
+    const float ms = to == -INFINITY ? 0.f : to, al = __builtin_amdgcn_exp2f(m - ms);
+    m = to;
+    l *= al;
+    y *= al;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int d = j * 64 + lane;
-      if (D % 64 == 0 || d < D) {
-        const float z = p[d];
-        y[j] += none ? 0.f : z * f;
-      }
+    for (int k = 0; k < AHEAD; ++k) {
+      // (a split without keys for the row leaves its sums unwritten)
+      if (x0 + k >= a.splits || (v[k].x == -INFINITY && v[k].y == 0.f)) continue;
+      const float f = __builtin_amdgcn_exp2f(v[k].x - ms);
+      l += v[k].y * f;
+      y += z[k] * f;
     }
   }
-  const float f = lt == 0.f ? 0.f : 1.f / lt;
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int d = j * 64 + lane;
-    if (D % 64 == 0 || d < D)
-      a.o[tok * a.o_stride + head * D + d] = __builtin_bit_cast(uint16_t, (E)(y[j] * f));
-  }
-  if (a.lse && lane == 0) a.lse[orow] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * LN2;
+  const float f = l == 0.f ? 0.f : 1.f / l;
+  *(uint2*)(a.o + (t.q0 + tok) * a.o_stride + head * D + d) = make_uint2(pack2<E>(y[0] * f, y[1] * f), pack2<E>(y[2] * f, y[3] * f));
+  if (a.lse && d == 0) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
 }
 
 template <class E, int D>
 hipError_t join_launch(const AttendArgs& a, hipStream_t st) {
   if (a.splits == 1) return hipSuccess;
-  attend_join_kernel<E, D><<<dim3((unsigned)((a.T * a.q_heads + 3) / 4)), 256, 0, st>>>(a);
+  attend_join_kernel<E, D><<<dim3((unsigned)(tile_count(a, join_rows(D)) * a.kv.kv_heads)), 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -597,16 +591,20 @@ AttendPlan attend_plan(const AttendArgs& a, int num_cu) {
   p.whole = span(p.stream_rows, AT_TILE) <= 4 * at_step(D);
   if (p.whole) p.splits = a.seqs;
   if (rows > most) {
-    // where every sequence has max_q rows (if cu_q says so too), all are the tile kernel's
-    if (a.T >= a.max_q * (int64_t)a.seqs) p.stream_rows = 0;
+    // All sequences are the tile kernel's where each has max_q rows (if cu_q
+    // says so too), and where so few keys are seen that a tile of few rows ends
+    // as soon as the others: one launch less (6 single tokens beside 6 chunks,
+    // 2047 keys: 13 us).
+    if (a.T >= a.max_q * (int64_t)a.seqs || span(128, 64) <= 4096) p.stream_rows = 0;
     // tiles of 256 rows where there are enough of them for every CU (of 96
     // dimensions the pieces cannot be dealt to 8 waves, and 256 take the
     // registers of two waves)
     const int64_t all = a.T * a.group;
     p.tile_rows = (D == 64 || D == 128) && all / 256 * hk >= num_cu ? 256 : 128;
     const int64_t tiles = ((all + p.tile_rows - 1) / p.tile_rows) * hk;
-    // (the grid has under 2^23 workgroups, those without rows among them)
-    const int64_t grid = (rows + p.tile_rows - 1) / p.tile_rows * hk * a.seqs, room = ((int64_t)1 << 23) / grid;
+    // as many splits as keep every workgroup on a CU from the beginning (the
+    // grid has under 2^23 workgroups, those without rows among them)
+    const int64_t room = ((int64_t)1 << 23) / (tile_count(a, p.tile_rows) * hk);
     int64_t want = 2 * num_cu / tiles;
     if (want > room) want = room;
     p.tile_splits = split_plan(span(p.tile_rows, 64), want, 512, 64, &p.tile_per);

@@ -71,10 +71,8 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
   b /= a.kv.kv_heads;
   const int split = b % a.splits;
   b /= a.splits;
-  const int tiles = a.tiles;
   RowTile t;
-  // the last rows see the most keys: they come first
-  if (!row_tile(a, b / tiles, hk, tiles - 1 - b % tiles, C::ROWS, a.stream_rows + 1, INT32_MAX, KT, t)) return;
+  if (!find_tile(a, b, hk, C::ROWS, KT, t)) return;
   int c0, c1;
   split_range(t, split, a.splits, a.per_split, c0, c1);
 
@@ -352,7 +350,7 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
   // 16-byte chunk c of row r at place c ^ (r & SWZ) of the row, for the banks
   constexpr int SWZ = D == 96 ? 3 : 7;
   static_assert(WAVES * 32 * D * 2 <= C::STAGES * C::STAGE, "rows fit");
-  uint8_t* s = smem + wave * 32 * D * 2;
+  uint8_t* mem = smem + wave * 32 * D * 2;
 #pragma unroll
   for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -360,7 +358,7 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
       uint2 z;
       z.x = pack2<E>(o[d][4 * x] * f, o[d][4 * x + 1] * f);
       z.y = pack2<E>(o[d][4 * x + 2] * f, o[d][4 * x + 3] * f);
-      *(uint2*)(s + r * (D * 2) + ((d * 4 + x) ^ (r & SWZ)) * 16 + h * 8) = z;
+      *(uint2*)(mem + r * (D * 2) + ((d * 4 + x) ^ (r & SWZ)) * 16 + h * 8) = z;
     }
   if (a.lse && h == 0 && there) a.lse[orow] = lt == 0.f ? -INFINITY : (m + log2f(lt)) * LN2;
   // (within a wave: LDS operations complete in order)
@@ -370,20 +368,18 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
     if (row2 < t.rows) {
       const int tok2 = row2 / a.group, head2 = hk * a.group + row2 - tok2 * a.group;
       *(u32x4*)(a.o + (t.q0 + tok2) * a.o_stride + head2 * D + c * 8) =
-          *(const u32x4*)(s + rr * (D * 2) + (c ^ (rr & SWZ)) * 16);
+          *(const u32x4*)(mem + rr * (D * 2) + (c ^ (rr & SWZ)) * 16);
     }
   }
 }
 
 template <class E, int D, int WAVES>
-hipError_t tile_launch(const AttendArgs& args, hipStream_t st) {
+hipError_t tile_launch(const AttendArgs& a, hipStream_t st) {
   using C = TileCfg<D, WAVES>;
   static std::atomic<uint64_t> raised{0};
   const hipError_t e = raise_lds_limit((const void*)attend_tile_kernel<E, D, WAVES>, C::LDS, raised);
   if (e != hipSuccess) return e;
-  AttendArgs a = args;
-  a.tiles = (int)(((int64_t)a.max_q * a.group + C::ROWS - 1) / C::ROWS);
-  const int64_t wgs = (int64_t)a.tiles * a.seqs * a.splits * a.kv.kv_heads;
+  const int64_t wgs = tile_count(a, C::ROWS) * a.splits * a.kv.kv_heads;
   attend_tile_kernel<E, D, WAVES><<<dim3((unsigned)wgs), WAVES * 64, C::LDS, st>>>(a);
   return hipGetLastError();
 }

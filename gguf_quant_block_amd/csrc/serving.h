@@ -69,7 +69,6 @@ struct AttendArgs {
   float* part;                // partial sums, and
   float* part_ml;             // their reference points and totals
   int splits, per_split;      // splits of the tile kernel; keys of a split
-  int tiles;                  // row tiles of a sequence (tile kernel)
   int stream_rows;            // most rows of a streamed sequence
   int shares;                 // workgroups of the streaming kernel for each key head
   bool whole;                 // each of them has a sequence of its own
