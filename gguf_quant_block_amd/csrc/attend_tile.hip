@@ -57,7 +57,9 @@ __device__ __forceinline__ void barrier_if(bool on) {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-template <class E, int D, int WAVES>
+// BIG: pages of KT keys or more, so that a tile is in one page and where it
+// begins is the same in every lane.
+template <class E, int D, int WAVES, bool BIG>
 __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kernel(AttendArgs a) {
   using C = TileCfg<D, WAVES>;
   static_assert(D / 8 % WAVES == 0, "pieces per wave");
@@ -104,28 +106,42 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
 #pragma unroll
     for (int x = 0; x < 16; ++x) o[d][x] = 0.f;
 
-  // Key tok0 + lane: its entry in the table (read a tile before it is looked
-  // at, so that nothing waits for it), its page, -1 for none of the pool (its
-  // keys take no part), and where the page begins in bytes.
+  // Key tok0 + lane (BIG: all of the tile's): its entry in the table (read a
+  // tile before it is looked at, so that nothing waits for it), its page, -1
+  // for none of the pool (its keys take no part), where the page begins in
+  // bytes, and which of the tile's keys have a page.
   auto entry_at = [&](int tok0) -> int {
-    const int key = tok0 + lane < c1 ? tok0 + lane : c1 - 1;
+    const int at = BIG ? tok0 : tok0 + lane, key = at < c1 ? at : c1 - 1;
     return *(const int32_t*)((const uint8_t*)table + (uint32_t)(key >> a.kv.page_shift) * 4u);
   };
   auto page_of = [&](int tok0, int entry) -> int {
-    return tok0 + lane < c1 && (unsigned)entry < (uint64_t)a.kv.pages ? entry : -1;
+    if constexpr (BIG) entry = __builtin_amdgcn_readfirstlane(entry);
+    return tok0 + (BIG ? 0 : lane) < c1 && (unsigned)entry < (uint64_t)a.kv.pages ? entry : -1;
   };
   auto start_of = [&](int page) -> uint64_t { return (uint32_t)(page < 0 ? 0 : page) * (uint64_t)(uint32_t)page_bytes; };
+  auto paged = [&](int tok0, int page) -> uint64_t {
+    if constexpr (!BIG) return __ballot(page >= 0);
+    return page < 0 ? 0 : (c1 - tok0 < KT ? ((uint64_t)1 << (c1 - tok0)) - 1 : ~0ull);
+  };
   // pieces of keys and of values on their way to LDS
   u32x4 kst[NI], vst[NI];
   auto load_k = [&](int tok0, uint64_t start) {
-    const uint8_t* kp = kbase + start + (((tok0 + lane) & (ps - 1)) * 16 + wave * NI * ps * 16);
+    if constexpr (BIG) {
+      const uint8_t* kp = kbase + start + (uint32_t)((tok0 & (ps - 1)) * 16 + wave * NI * ps * 16);
 #pragma unroll
-    for (int i = 0; i < NI; ++i) kst[i] = *(const u32x4*)(kp + (uint32_t)(i * ps * 16));
+      for (int i = 0; i < NI; ++i) kst[i] = *(const u32x4*)(kp + (uint32_t)(i * ps * 16) + (uint32_t)lane * 16);
+    } else {
+      const uint8_t* kp = kbase + start + (((tok0 + lane) & (ps - 1)) * 16 + wave * NI * ps * 16);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) kst[i] = *(const u32x4*)(kp + (uint32_t)(i * ps * 16));
+    }
   };
   auto load_v = [&](int tok0, uint64_t start) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      if constexpr (D % 64 == 0) {               // the wave's 64 pieces are of the same 8 keys
+      if constexpr (BIG) {                       // pieces of a page follow each other
+        vst[i] = *(const u32x4*)(vbase + start + (uint32_t)((tok0 & (ps - 1)) * (D * 2) + (wave * NI + i) * 1024) + (uint32_t)lane * 16);
+      } else if constexpr (D % 64 == 0) {        // the wave's 64 pieces are of the same 8 keys
         const int p = (wave * NI + i) * 64, k8 = p / D, d = p - k8 * D;
         const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(start >> 32), k8 * 8) << 32 |
                             (uint32_t)__builtin_amdgcn_readlane((int)start, k8 * 8);
@@ -252,7 +268,7 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
     const int p0 = page_of(c0, entry_at(c0)), p1 = page_of(c0 + KT, entry_at(c0 + KT));
     const int p2 = page_of(c0 + 2 * KT, entry_at(c0 + 2 * KT));
     int e3 = entry_at(c0 + 3 * KT);
-    uint64_t ok = __ballot(p0 >= 0), ok1 = __ballot(p1 >= 0), ok2 = __ballot(p2 >= 0), start2 = start_of(p2);
+    uint64_t ok = paged(c0, p0), ok1 = paged(c0 + KT, p1), ok2 = paged(c0 + 2 * KT, p2), start2 = start_of(p2);
     load_k(c0, start_of(p0));
     store(C::KB, kst);
     load_v(c0, start_of(p0));
@@ -269,7 +285,7 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
     int cur = C::STAGE, next = C::STAGES == 2 ? 0 : 2 * C::STAGE;
     for (int tok0 = c0; tok0 < c1; tok0 += KT) {
       const int p3 = page_of(tok0 + 3 * KT, e3);
-      const uint64_t ok3 = __ballot(p3 >= 0), start3 = start_of(p3);
+      const uint64_t ok3 = paged(tok0 + 3 * KT, p3), start3 = start_of(p3);
       weights(tok0, ok);
       half_barrier();
       // (past the last tile the loads are of keys without a page, never read)
@@ -302,7 +318,7 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
   if (c0 < c1 && *flag) {                        // (all waves have passed the loop's last barrier)
     for (int tok0 = c0; tok0 < c1; tok0 += KT) {
       const int page = page_of(tok0, entry_at(tok0));
-      const uint64_t ok = __ballot(page >= 0);
+      const uint64_t ok = paged(tok0, page);
       if (is_open(tok0, ok, t.lo, t.hi)) continue;
       const int in_page = tok0 & (ps - 1);
 #pragma unroll
@@ -314,7 +330,7 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
         for (int s = 0; s < 4; ++s) {
           const int key0 = tok0 + s * 16 + 8 * h, n = have(tok0, ok, 2 * s + h);
           const u32x4 one = seen_ones<E>(pos - key0 < n ? pos - key0 : n - 1, a.window > 0 ? pos - a.window - key0 : -1);
-          const int pg = __shfl(page, s * 16 + 8 * h);
+          const int pg = BIG ? page : __shfl(page, s * 16 + 8 * h);
           const u32x4 v = *(const u32x4*)(vbase + start_of(pg) +
                                           ((((in_page + s * 16 + 8 * h) & (ps - 1)) >> 3) * D + d * 32 + r) * 16);
           c = Mat<E>::mfma32(nonfinite_codes<E>(v & keep_keys(n)), one, c);
@@ -373,22 +389,27 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
   }
 }
 
-template <class E, int D, int WAVES>
+template <class E, int D, int WAVES, bool BIG>
 hipError_t tile_launch(const AttendArgs& a, hipStream_t st) {
   using C = TileCfg<D, WAVES>;
   static std::atomic<uint64_t> raised{0};
-  const hipError_t e = raise_lds_limit((const void*)attend_tile_kernel<E, D, WAVES>, C::LDS, raised);
+  const hipError_t e = raise_lds_limit((const void*)attend_tile_kernel<E, D, WAVES, BIG>, C::LDS, raised);
   if (e != hipSuccess) return e;
   const int64_t wgs = tile_count(a, C::ROWS) * a.splits * a.kv.kv_heads;
-  attend_tile_kernel<E, D, WAVES><<<dim3((unsigned)wgs), WAVES * 64, C::LDS, st>>>(a);
+  attend_tile_kernel<E, D, WAVES, BIG><<<dim3((unsigned)wgs), WAVES * 64, C::LDS, st>>>(a);
   return hipGetLastError();
+}
+
+template <class E, int D, int WAVES>
+hipError_t tile_w(const AttendArgs& a, hipStream_t st) {
+  return (1 << a.kv.page_shift) >= KT ? tile_launch<E, D, WAVES, true>(a, st) : tile_launch<E, D, WAVES, false>(a, st);
 }
 
 template <class E, int D>
 hipError_t tile_d(const AttendArgs& a, const AttendPlan& p, hipStream_t st) {
   if constexpr (D == 64 || D == 128)
-    if (p.tile_rows == 256) return tile_launch<E, D, 8>(a, st);
-  return tile_launch<E, D, 4>(a, st);
+    if (p.tile_rows == 256) return tile_w<E, D, 8>(a, st);
+  return tile_w<E, D, 4>(a, st);
 }
 
 template <class E>
