@@ -596,18 +596,25 @@ AttendPlan attend_plan(const AttendArgs& a, int num_cu) {
     // as soon as the others: one launch less (6 single tokens beside 6 chunks,
     // 2047 keys: 13 us).
     if (a.T >= a.max_q * (int64_t)a.seqs || span(128, 64) <= 4096) p.stream_rows = 0;
-    // tiles of 256 rows where there are enough of them for every CU (of 96
-    // dimensions the pieces cannot be dealt to 8 waves, and 256 take the
-    // registers of two waves)
+    // Tiles of 256 rows take half the LDS traffic of two of 128, but fill
+    // fewer CUs: where there is one for every CU, or where the keys are long
+    // enough to be split (128 rows and 256, us: 64 tokens over 30000 keys, 4
+    // query heads for each of 8: 69 and 63; 1000 over 4000: 72 and 61; 2000
+    // over 2000: 71 and 74; 600 over 600: 23 and 28).  Not of 96 dimensions,
+    // whose pieces cannot be dealt to 8 waves, nor of 256, which take the
+    // registers of two waves.
     const int64_t all = a.T * a.group;
-    p.tile_rows = (D == 64 || D == 128) && all / 256 * hk >= num_cu ? 256 : 128;
+    const bool wide = all / 256 * hk >= num_cu || (rows >= 192 && span(256, 64) >= 3600);
+    p.tile_rows = (D == 64 || D == 128) && wide ? 256 : 128;
     const int64_t tiles = ((all + p.tile_rows - 1) / p.tile_rows) * hk;
-    // as many splits as keep every workgroup on a CU from the beginning (the
-    // grid has under 2^23 workgroups, those without rows among them)
+    // Splits for a workgroup per CU (two: 84 us for the 69 above), of 768
+    // keys or more: joining takes about 10 us, a tile of 64 keys 1.5 (600 over
+    // 600: 23 us, in two splits 34).  The grid has under 2^23 workgroups,
+    // those without rows among them.
     const int64_t room = ((int64_t)1 << 23) / (tile_count(a, p.tile_rows) * hk);
-    int64_t want = 2 * num_cu / tiles;
+    int64_t want = (num_cu + tiles / 2) / tiles;
     if (want > room) want = room;
-    p.tile_splits = split_plan(span(p.tile_rows, 64), want, 512, 64, &p.tile_per);
+    p.tile_splits = split_plan(span(p.tile_rows, 64), want, 768, 64, &p.tile_per);
   }
   return p;
 }
