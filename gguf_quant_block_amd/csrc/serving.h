@@ -69,18 +69,18 @@ struct AttendArgs {
   float* part;                // partial sums, and
   float* part_ml;             // their reference points and totals
   int splits, per_split;      // splits of the tile kernel; keys of a split
-  int stream_rows;            // most rows of a streamed sequence
+  int stream_rows;            // most rows of a streamed sequence; 0: none is streamed
   int shares;                 // workgroups of the streaming kernel for each key head
   bool whole;                 // each of them has a sequence of its own
   uint32_t* arrived;          // [seqs][kv_heads] pieces of a sequence that are there; 0 between calls
   int64_t counters;           // entries of `arrived`
   bool fresh;                 // they are to be cleared first
 };
-// Sequences with at most AT_STREAM_ROWS rows (tokens times the group) for each
+// Sequences with at most stream_rows rows (tokens times the group) for each
 // key head are the streaming kernel's, the others the tile kernel's; the
 // lengths are known on the device only, so where max_q allows both, both are
 // launched and a workgroup without rows of its kind ends at once.
-constexpr int AT_STREAM_ROWS = 32;
+constexpr int AT_STREAM_ROWS = 32;   // at most; 16 with 256 dimensions
 struct AttendPlan {
   int stream_rows;            // most rows of a streamed sequence
   int splits;                 // shares of the streaming kernel
