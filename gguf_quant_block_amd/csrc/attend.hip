@@ -606,18 +606,19 @@ AttendPlan attend_plan(const AttendArgs& a, int num_cu) {
     // Tiles of 256 rows take half the LDS traffic of two of 128, but fill
     // fewer CUs: where there is one for every CU, or where the keys are long
     // enough to be split (128 rows and 256, us: 64 tokens over 30000 keys, 4
-    // query heads for each of 8: 69 and 63; 1000 over 4000: 72 and 61; 2000
-    // over 2000: 71 and 74; 600 over 600: 23 and 28).  Not of 96 dimensions,
-    // whose pieces cannot be dealt to 8 waves, nor of 256, which take the
-    // registers of two waves.
+    // query heads for each of 8: 69 and 61; twice 2048 over 4096, one query
+    // head: 99 and 91; 2000 over 2000: 67 and 67; 600 over 600: 24 and 26).
+    // Not of 96 dimensions, whose pieces cannot be dealt to 8 waves, nor of
+    // 256, which take the registers of two waves.
     const int64_t all = a.T * a.group;
     const bool wide = all / 256 * hk >= num_cu || (rows >= 192 && span(256, 64) >= 3600);
     p.tile_rows = (D == 64 || D == 128) && wide ? 256 : 128;
     const int64_t tiles = ((all + p.tile_rows - 1) / p.tile_rows) * hk;
-    // Splits for a workgroup per CU (two: 84 us for the 69 above), of 768
-    // keys or more: joining takes about 10 us, a tile of 64 keys 1.5 (600 over
-    // 600: 23 us, in two splits 34).  The grid has under 2^23 workgroups,
-    // those without rows among them.
+    // Splits for a workgroup per CU (two: chunks beside single tokens with a
+    // window 47 us instead of 41, 8 sequences of up to 1000 keys 29 instead of
+    // 25, 30000 keys 68 instead of 69), of 768 keys or more: joining takes 5 to
+    // 10 us, a tile of 64 keys 1.5 (600 over 600: 24 us, in two splits 28).
+    // The grid has under 2^23 workgroups, those without rows among them.
     const int64_t room = ((int64_t)1 << 23) / (tile_count(a, p.tile_rows) * hk);
     int64_t want = (num_cu + tiles / 2) / tiles;
     if (want > room) want = room;

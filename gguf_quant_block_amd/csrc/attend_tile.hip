@@ -23,8 +23,8 @@
 //
 // Bound by the matrix and vector instructions of a wave's 32 rows, and by the
 // clock that the card holds under them: 4096 tokens over 8192 keys (32 heads
-// of 128 on 8 key heads, f16) take 415 to 447 us on different cards, 920 to
-// 995 TFLOP/s, where a product of two 8192 x 8192 matrices reaches 1200; the
+// of 128 on 8 key heads, f16) take 401 to 421 us on different cards, 980 to
+// 1025 TFLOP/s, where a product of two 8192 x 8192 matrices reaches 1200; the
 // matrix cores are busy for 397 of 914 thousand cycles, at 1.8 to 2.1 GHz.
 // The same with 4 waves of 64 rows spilled (454 TFLOP/s), and without the
 // halves' offset (below) took 4 % longer.  The weights are rounded to the
@@ -45,9 +45,8 @@ struct TileCfg {
   static constexpr int ROWS = WAVES * 32;
   static constexpr int KB = KT * D * 2;          // bytes of a tile's keys, and of its values
   static constexpr int STAGE = 2 * KB;           // values of a tile, then keys of the next
-  static constexpr int STAGES = D <= 128 ? 3 : 2;
+  static constexpr int STAGES = WAVES > 4 ? 3 : 2;   // (a wave that runs behind needs a third)
   static constexpr int LDS = STAGES * STAGE + 16;
-  static_assert(STAGES == 3 || WAVES == 4, "a wave behind needs a third stage");
   static constexpr int NI = D / 8 / WAVES;       // 1 KB pieces of keys per wave
 };
 
@@ -273,8 +272,8 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
   // Of the loop's two halves one is vector work (weights), one matrix work.
   // With 8 waves, waves 4 to 7 run one half behind waves 0 to 3, their
   // neighbours on the SIMDs, so that one of the two kinds of work is always
-  // next to the other.  Stage n is stored in the second halves of tile n - 2 and
-  // read in those of tile n - 1.
+  // next to the other.  Stage n is stored at the end of the first halves of tile
+  // n - 2 and read in the second halves of tile n - 1.
   if (c0 < c1) {
     const int p0 = page_of(c0, entry_at(c0)), p1 = page_of(c0 + KT, entry_at(c0 + KT));
     const int p2 = page_of(c0 + 2 * KT, entry_at(c0 + 2 * KT));
@@ -298,11 +297,12 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
       const int p3 = page_of(tok0 + 3 * KT, e3);
       const uint64_t ok3 = paged(tok0 + 3 * KT, p3), start3 = start_of(p3);
       weights(tok0, ok);
-      half_barrier();
-      // (past the last tile the loads are of keys without a page, never read)
+      __builtin_amdgcn_sched_barrier(0);
       clean(tok0 + KT, ok1);
       store(next, vst);
       store(next + C::KB, kst);
+      half_barrier();
+      // (past the last tile the loads are of keys without a page, never read)
       load_v(tok0 + 2 * KT, start2);
       load_k(tok0 + 3 * KT, start3);
       e3 = entry_at(tok0 + 4 * KT);
