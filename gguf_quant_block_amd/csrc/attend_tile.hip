@@ -179,7 +179,7 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
   // ok: bit j: key tok0 + j has a page
   // every row from position lo to hi sees every key of the tile: no mask
   auto is_open = [&](int tok0, uint64_t ok, int lo, int hi) {
-    return ok == ~0ull && tok0 + KT - 1 <= lo && (a.window <= 0 || tok0 > hi - a.window);
+    return ok == ~0ull && tok0 <= lo - (KT - 1) && tok0 > (a.window > 0 ? hi - a.window : -1);
   };
   // how many of the tile's keys 8x .. 8x + 7 are there (the first ones)
   auto have = [&](int tok0, uint64_t ok, int x) -> int {
