@@ -107,7 +107,12 @@ __device__ __forceinline__ u32x4 keep_keys(int n) {
   for (int j = 0; j < 4; ++j) k[j] = n > 2 * j + 1 ? 0xFFFFFFFFu : (n == 2 * j + 1 ? 0xFFFFu : 0u);
   return k;
 }
-// clears the non-finite values; not 0 if there were any
+// not 0 if there are non-finite values
+template <class E>
+__device__ __forceinline__ uint32_t any_nonfinite(u32x4 v) {
+  return nonfinite2<E>(v[0]) | nonfinite2<E>(v[1]) | nonfinite2<E>(v[2]) | nonfinite2<E>(v[3]);
+}
+// clears them; not 0 if there were any
 template <class E>
 __device__ __forceinline__ uint32_t take_nonfinite(u32x4& v) {
   uint32_t bad = 0;

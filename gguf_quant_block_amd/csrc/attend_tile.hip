@@ -190,13 +190,17 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
   // of tiles with masked keys those are stored as 0 and added at the end.
   auto clean = [&](int tok0, uint64_t ok) {
     if (is_open(tok0, ok, t.lo, t.hi)) return;
+    if (ok != ~0ull)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) vst[i] &= keep_keys(have(tok0, ok, ((wave * NI + i) * 64 + lane) / D));
     uint32_t bad = 0;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      vst[i] &= keep_keys(have(tok0, ok, ((wave * NI + i) * 64 + lane) / D));
-      bad |= take_nonfinite<E>(vst[i]);
+    for (int i = 0; i < NI; ++i) bad |= any_nonfinite<E>(vst[i]);
+    if (__any(bad != 0)) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) take_nonfinite<E>(vst[i]);
+      *flag = 1;
     }
-    if (bad) *flag = 1;
   };
 
   floatx16 sc[2];                            // scores
