@@ -617,12 +617,15 @@ AttendPlan attend_plan(const AttendArgs& a, int num_cu) {
     // Splits for a workgroup per CU (two: chunks beside single tokens with a
     // window 47 us instead of 41, 8 sequences of up to 1000 keys 29 instead of
     // 25, 30000 keys 68 instead of 69), of 768 keys or more: joining takes 5 to
-    // 10 us, a tile of 64 keys 1.5 (600 over 600: 24 us, in two splits 28).
+    // 10 us, a tile of 64 keys 1.5 (600 over 600: 24 us, in two splits 28);
+    // of 256 where those would leave half of the CUs idle (twice 11 tokens
+    // over 5645 keys of 256 dimensions: 49 us and 36).
     // The grid has under 2^23 workgroups, those without rows among them.
     const int64_t room = ((int64_t)1 << 23) / (tile_count(a, p.tile_rows) * hk);
     int64_t want = (num_cu + tiles / 2) / tiles;
     if (want > room) want = room;
-    p.tile_splits = split_plan(span(p.tile_rows, 64), want, 768, 64, &p.tile_per);
+    const int64_t few = tiles * ((span(p.tile_rows, 64) + 767) / 768) < num_cu / 2;
+    p.tile_splits = split_plan(span(p.tile_rows, 64), want, few ? 256 : 768, 64, &p.tile_per);
   }
   return p;
 }
