@@ -10,8 +10,8 @@
 // share it, token by token, so that K and V are read once for all of them.
 // With up to 32 rows the kernel is bound by HBM (the keys and values); the
 // matrix instructions cost less than the loads even with one row of 16 in use.
-// Measured: one token over 131072 keys (32 heads of 128 on 8 key heads) 98 us,
-// 5.5 TB/s; 64 tokens over up to 8192 keys each 137 us, 5.4 TB/s, of 6.1 that
+// Measured: one token over 131072 keys (32 heads of 128 on 8 key heads) 99 us,
+// 5.4 TB/s; 64 tokens over up to 8192 keys each 137 us, 5.4 TB/s, of 6.1 that
 // a plain read of 1 GiB reaches; bytes from HBM 1.005 of the keys and values.
 // Short calls are bound by latency: 8 x 5 drafted tokens over up to 6001 keys
 // 28 us (15 us at 5.3 TB/s, then 7 us for the pieces to be joined), one token
@@ -481,8 +481,8 @@ __global__ __launch_bounds__(at_waves(D) * 64, at_waves(D) / 4) void attend_stre
 }
 
 // Joins the splits of the tile kernel: four columns of a row are a thread's,
-// in one pass with a running maximum.  Bound by latency (5 us for 2100 tokens
-// of 16 heads in two splits).
+// in one pass with a running maximum.  Bound by latency (5 us for 1193 tokens
+// of 16 heads of 64 in two splits).
 constexpr int join_rows(int D) { return 1024 / D; }   // of a workgroup
 template <class E, int D>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
@@ -600,7 +600,7 @@ AttendPlan attend_plan(const AttendArgs& a, int num_cu) {
   if (rows > most) {
     // All sequences are the tile kernel's where each has max_q rows (if cu_q
     // says so too), and where so few keys are seen that a tile of few rows ends
-    // as soon as the others: one launch less (6 single tokens beside 6 chunks,
+    // as soon as the others: one launch less (7 short sequences beside chunks,
     // 2047 keys: 13 us).
     if (a.T >= a.max_q * (int64_t)a.seqs || span(128, 64) <= 4096) p.stream_rows = 0;
     // Tiles of 256 rows take half the LDS traffic of two of 128, but fill

@@ -23,11 +23,10 @@
 //
 // Bound by the matrix and vector instructions of a wave's 32 rows, and by the
 // clock that the card holds under them: 4096 tokens over 8192 keys (32 heads
-// of 128 on 8 key heads, f16) take 401 to 421 us on different cards, 980 to
-// 1025 TFLOP/s, where a product of two 8192 x 8192 matrices reaches 1200; the
-// matrix cores are busy for 397 of 914 thousand cycles, at 1.8 to 2.1 GHz.
-// The same with 4 waves of 64 rows spilled (454 TFLOP/s), and without the
-// halves' offset (below) took 4 % longer.  The weights are rounded to the
+// of 128 on 8 key heads, f16) take 396 to 421 us on different cards, 980 to
+// 1040 TFLOP/s, where a product of two 8192 x 8192 matrices reaches 1200; the
+// matrix cores are busy for 397 of 798 thousand cycles, at about 2 GHz.  4
+// waves of 64 rows spilled (454 TFLOP/s).  The weights are rounded to the
 // cache's type for the second product; totals, products and statistics are
 // f32, the totals of the unrounded weights.
 #include <math.h>
