@@ -157,8 +157,10 @@ __global__ __launch_bounds__(AP_THREADS) void kv_append_kernel(AppendArgs a) {
     if (z.u < rot_units) rotate8<E>(y0, y1, cs + z.t * half + z.u * 8, a.interleaved);
     if (z.h < a.q_heads) {
       uint16_t* dst = a.q_out + (t0 + z.t) * a.o_stride + z.h * D;
-      *(u32x4*)(dst + z.p0 * 8) = y0;
-      *(u32x4*)(dst + z.p1 * 8) = y1;
+      // (past the caches: whole lines that others read next, on other XCDs;
+      // 31.7 -> 28.9 us for the 4096 tokens where nothing is in a cache yet)
+      __builtin_nontemporal_store(y0, (u32x4*)(dst + z.p0 * 8));
+      __builtin_nontemporal_store(y1, (u32x4*)(dst + z.p1 * 8));
     } else if (s >= 0) {
       uint16_t* dst = (uint16_t*)a.kv.k + (int64_t)(s >> a.kv.page_shift) * page_elems +
                       (int64_t)(z.h - a.q_heads) * ps * D + (s & (ps - 1)) * 8;
