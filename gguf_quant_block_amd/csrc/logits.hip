@@ -133,7 +133,8 @@ __global__ __launch_bounds__(LG_THREADS) void logits_kernel(LogitsArgs a) {
       if (biased) f += bias[i + e];
       out[e] = (O)(allow[k] >> e & 1 ? f : -INFINITY);
     }
-    if (i + V <= n) *(OV*)(y + i) = out;
+    // (past the caches: 34.5 -> 32.5 us for 128 rows of which nothing is cached)
+    if (i + V <= n) __builtin_nontemporal_store(out, (OV*)(y + i));
     else
 #pragma unroll
       for (int e = 0; e < V; ++e)
