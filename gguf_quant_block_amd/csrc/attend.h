@@ -90,6 +90,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// The reference point of a row's exponentials: the largest score in powers of
+// two, less LIFT.  (Not fused: the fused form keeps LIFT in a register.)
+template <class E>
+__device__ __forceinline__ float reference_of(float mx, float scale_log2) {
+#pragma clang fp contract(off)
+  const float z = mx * scale_log2;
+  return z - Mat<E>::LIFT;
+}
+
 // ---- values in masked places ----
 //
 // A masked key's weight is 0, and 0 times an infinite or NaN value would be

@@ -2,7 +2,7 @@
 // query rows for each key head) and the split of the work.
 //
 //   row (token i of sequence s, head): position p = kv_len - q_len + i
-//   o = sum_j 2^(c q.k_j - m) v_j / l,   m = max_j c q.k_j,  l = sum_j 2^(c q.k_j - m)
+//   o = sum_j 2^(c q.k_j - m) v_j / l,   m = max_j c q.k_j - LIFT,  l = sum_j 2^(c q.k_j - m)
 // over the keys j <= p, j > p - window, on pages of the pool; c = scale log2(e).
 // One pass: m and l run along, and the sums are scaled when m grows.
 //
@@ -28,8 +28,10 @@
 // requested as soon as this tile's scores exist, its values after the sums.
 //
 // The weights are rounded to the cache's type for the second product (f16 or
-// bf16 matrix instructions); the totals are summed in f32 from the unrounded
-// weights, and products, sums and statistics are f32.
+// bf16 matrix instructions): off by half a step, 2^-8 of a bf16 weight, 2^-11 of
+// an f16 one or 2^-33 of the row's largest (LIFT in serving.h).  The totals are
+// summed in f32 from the unrounded weights, and products, sums and statistics
+// are f32.
 #include <math.h>
 
 #include "attend.h"
@@ -166,7 +168,7 @@ struct Piece {
         for (int j = 1; j < 4; ++j) mx = max3(mx, sc[i][0][j], sc[i][1][j]);
         mx = fmaxf(mx, __shfl_xor(mx, 16));
         mx = fmaxf(mx, __shfl_xor(mx, 32));
-        const float mn = fmaxf(m[i], mx * a.scale_log2);
+        const float mn = fmaxf(m[i], reference_of<E>(mx, a.scale_log2));
         const float ms = mn == -INFINITY ? 0.f : mn;
         const float al = __builtin_amdgcn_exp2f(m[i] - ms);
         m[i] = mn;

@@ -15,11 +15,13 @@
 // [8][D] of values) whatever the page size, and every LDS read is a
 // contiguous 1024 bytes.
 //
-// The reference point m of a row's exponentials is a maximum of some earlier
-// tile.  A tile's weights are taken against it as it stands; only if their sum
-// then passes MOST (or m is still -inf) is the tile's maximum looked for, m
-// moved and the weights taken again.  Weights stay below MOST, in range of
-// f16, and most tiles cost no maximum and leave the sums as they are.
+// The reference point m of a row's exponentials is LIFT below a maximum of some
+// earlier tile.  A tile's weights are taken against it as it stands; only if
+// their sum then passes MOST (or m is still -inf) is the tile's maximum looked
+// for, m moved and the weights taken again.  Weights stay below MOST, in range
+// of f16, and most tiles cost no maximum and leave the sums as they are (f16:
+// 32 equal weights of a lane make 2^13, so that scores may grow by 3 to 8
+// powers of two before m moves).
 //
 // Bound by the matrix and vector instructions of a wave's 32 rows, and by the
 // clock that the card holds under them: 4096 tokens over 8192 keys (32 heads
@@ -27,8 +29,9 @@
 // 1040 TFLOP/s, where a product of two 8192 x 8192 matrices reaches 1200; the
 // matrix cores are busy for 397 of 798 thousand cycles, at about 2 GHz.  4
 // waves of 64 rows spilled (454 TFLOP/s).  The weights are rounded to the
-// cache's type for the second product; totals, products and statistics are
-// f32, the totals of the unrounded weights.
+// cache's type for the second product (off by 2^-8 of a bf16 weight, by 2^-11 of
+// an f16 one or 2^-33 of the row's largest); totals, products and statistics
+// are f32, the totals of the unrounded weights.
 #include <math.h>
 
 #include "attend.h"
@@ -37,7 +40,6 @@ namespace fcg {
 namespace {
 
 constexpr int KT = 64;                           // keys of a tile
-constexpr float MOST = 4096.f;
 
 template <int D, int WAVES>
 struct TileCfg {
@@ -244,12 +246,12 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
       return sum[0] + sum[1];
     };
     float sum = take(m);
-    if (__any(!(sum <= MOST))) {               // (m = -inf makes it infinite or NaN)
+    if (__any(!(sum <= Mat<E>::MOST))) {               // (m = -inf makes it infinite or NaN)
       float mx = fmaxf(sc[0][0], sc[1][0]);
 #pragma unroll
       for (int x = 1; x < 16; ++x) mx = max3(mx, sc[0][x], sc[1][x]);
       mx = fmaxf(mx, other_half(mx));
-      const float to = fmaxf(m, mx * a.scale_log2), ms = to == -INFINITY ? 0.f : to;
+      const float to = fmaxf(m, reference_of<E>(mx, a.scale_log2)), ms = to == -INFINITY ? 0.f : to;
       const float al = __builtin_amdgcn_exp2f(m - ms);
       m = to;
       l *= al;

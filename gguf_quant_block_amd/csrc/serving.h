@@ -119,6 +119,13 @@ template <> struct Mat<f16> {
   typedef f16 x8 __attribute__((ext_vector_type(8)));
   static constexpr uint32_t EXP1 = 0x04000400u;   // one exponent step in both halves of a dword
   static constexpr uint32_t INF = 0x7C00u, ONE = 0x3C00u, TWO7 = 0x5800u, TWO14 = 0x7400u;
+  // Attention's weights are taken against the largest score less LIFT: up to
+  // 2^LIFT, so that the rounding to f16, absolute below its normal range,
+  // keeps what many small weights beside a large one hold (2^-33 of the
+  // largest; of 2^-25, 2500 keys of 2^-25 each lost all of it).  Sums of
+  // several weights stay finite.
+  static constexpr float LIFT = 8.f;
+  static constexpr float MOST = 65504.f;          // largest finite value
   static __device__ __forceinline__ floatx4 mfma16(u32x4 a, u32x4 b, floatx4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
   }
@@ -130,6 +137,8 @@ template <> struct Mat<bf16> {
   typedef bf16 x8 __attribute__((ext_vector_type(8)));
   static constexpr uint32_t EXP1 = 0x00800080u;
   static constexpr uint32_t INF = 0x7F80u, ONE = 0x3F80u, TWO7 = 0x4300u, TWO14 = 0x4680u;
+  static constexpr float LIFT = 0.f;              // (f32's exponents: 2^-133)
+  static constexpr float MOST = 4096.f;
   static __device__ __forceinline__ floatx4 mfma16(u32x4 a, u32x4 b, floatx4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
   }
