@@ -33,7 +33,8 @@ CFLAGS = [
     "-Wno-unused-command-line-argument",
 ]
 SOURCES = ["fc_gguf_api.cpp", "layout.hip", "gemv.hip", "prefill.hip", "skinny.hip", "prefill_i8.hip",
-           "moe.hip", "dequant.hip", "serving_api.cpp", "kv_append.hip", "attend.hip", "attend_tile.hip", "logits.hip"]
+           "moe.hip", "dequant.hip", "serving_api.cpp", "attend_plan.cpp", "kv_append.hip", "attend.hip", "attend_tile.hip",
+           "logits.hip"]
 CEIL_SOURCES = ["ceilings.hip"]
 
 

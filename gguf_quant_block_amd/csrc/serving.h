@@ -80,7 +80,12 @@ struct AttendArgs {
 // key head are the streaming kernel's, the others the tile kernel's; the
 // lengths are known on the device only, so where max_q allows both, both are
 // launched and a workgroup without rows of its kind ends at once.
-constexpr int AT_STREAM_ROWS = 32;   // at most; 16 with 256 dimensions
+constexpr int at_stream_rows(int D) { return D == 256 ? 16 : 32; }   // at most (two row tiles of 256 dimensions do not fit a wave's registers)
+// The streaming kernel: keys per wave and step, and waves of a workgroup, 8
+// (two on each SIMD, of 256 registers) or 4 where a wave needs more.
+constexpr int AT_TILE = 32;
+constexpr int at_waves(int D) { return D == 256 ? 4 : 8; }
+constexpr int at_step(int D) { return at_waves(D) * AT_TILE; }
 struct AttendPlan {
   int stream_rows;            // most rows of a streamed sequence
   int splits;                 // shares of the streaming kernel
@@ -89,8 +94,36 @@ struct AttendPlan {
   int tile_splits, tile_per;
 };
 AttendPlan attend_plan(const AttendArgs& a, int num_cu);
+size_t attend_part_rows(const AttendArgs& a, const AttendPlan& p);
 size_t attend_workspace_bytes(const AttendArgs& a, const AttendPlan& p);
 hipError_t launch_attend(const AttendArgs& a, const AttendPlan& p, int dtype, hipStream_t st);
+
+// A bound of attend_workspace_bytes over this call and all that are smaller in
+// T, seqs, max_q, table width and heads, whatever their windows: a workspace
+// of these bytes serves them all, though a smaller call may need more than a
+// larger one (4096 tokens fill the CUs unsplit, 64 need 34 MB).
+inline size_t attend_workspace_bound(const AttendArgs& a, int num_cu) {
+  const int64_t D = a.kv.head_dim, hk = a.kv.kv_heads, held = (int64_t)a.table_w << a.kv.page_shift;
+  const int64_t rows = (int64_t)a.max_q * a.group, step = at_step((int)D), few = at_stream_rows((int)D);
+  int64_t stream = 0, tile = 0;
+  if (held > 4 * step) {                         // shares of the streaming kernel: one a CU, one a step
+    const int64_t steps = (held + step - 1) / step * a.seqs;
+    int64_t shares = num_cu / hk < steps ? num_cu / hk : steps;
+    shares = shares < 1 ? 1 : shares;
+    stream = shares * hk * 2 * (rows < few ? rows : few);
+  }
+  // Splits of the tile kernel: of 256 keys at least; about num_cu / tiles,
+  // rounded, of 2 tiles for 3 CUs at most, so that all splits have 4/3 num_cu
+  // tiles at most; tiles of 256 rows only where the plan may split those.
+  const int64_t most = (num_cu + hk / 2) / hk, by_keys = (held + 255) / 256;
+  const int64_t splits = most < by_keys ? most : by_keys;
+  if (rows > few && splits > 1) {
+    const int64_t by_rows = splits * a.T * a.q_heads;
+    const int64_t by_tiles = (num_cu + num_cu / 3) * (int64_t)((D == 64 || D == 128) && rows >= 192 && held >= 3600 ? 256 : 128);
+    tile = by_rows < by_tiles ? by_rows : by_tiles;
+  }
+  return (size_t)(stream > tile ? stream : tile) * (D + 2) * sizeof(float);
+}
 
 struct LogitsArgs {
   const void* x;              // [rows][x_stride]

@@ -14,6 +14,12 @@
 #include "fc_gguf.h"
 #include "serving.h"
 
+// A workspace that a captured graph uses, kept until the handle goes.
+struct KeptWorkspace {
+  void* p;
+  KeptWorkspace* next;
+};
+
 struct fc_gguf_kv {
   fcg::KvPages kv = {};
   int dtype = 0;
@@ -23,6 +29,8 @@ struct fc_gguf_kv {
   size_t ws_bytes = 0;
   int64_t counters = 0;
   bool fresh = false;           // the counters are to be cleared by the next call
+  bool graphed = false;         // a captured call uses it
+  KeptWorkspace* kept = nullptr;
 };
 
 namespace {
@@ -56,33 +64,51 @@ int check_kv_device(const fc_gguf_kv* h) {
 
 size_t counter_bytes(int64_t counters) { return ((size_t)counters * 4 + 255) / 256 * 256; }
 
-// Grows the workspace (counters, then `bytes`) on the call's stream: released
-// to and taken from the device's stream-ordered pool, so that the growth waits
-// for that stream only.  Not while the stream is captured: the memory would
-// belong to the graph.
-int ensure_kv_ws(fc_gguf_kv* h, int64_t counters, size_t bytes, hipStream_t st) {
-  if (counters <= h->counters && counter_bytes(h->counters) + bytes <= h->ws_bytes) return FC_GGUF_OK;
+// Sees to a workspace of `counters` and `need` bytes.  Outside a capture it is
+// made large enough for `bound` bytes, which no smaller call exceeds, so that
+// smaller calls never move it.  It grows on the call's stream: released to and
+// taken from the device's stream-ordered pool, so that the growth waits for
+// that stream only.  One that a captured call uses is not released but kept for
+// the graph, whose launches leave its counters at 0.  While the stream is
+// captured nothing grows: the memory would belong to the graph.
+int ensure_kv_ws(fc_gguf_kv* h, int64_t counters, size_t need, size_t bound, hipStream_t st, bool* in_capture) {
+  *in_capture = false;
+  if (bound == 0) return FC_GGUF_OK;
+  auto holds = [&](size_t bytes) { return counters <= h->counters && counter_bytes(h->counters) + bytes <= h->ws_bytes; };
   hipStreamCaptureStatus captured = hipStreamCaptureStatusNone;
-  if (hipStreamIsCapturing(st, &captured) == hipSuccess && captured != hipStreamCaptureStatusNone) return FC_GGUF_ENOMEM;
+  if (hipStreamIsCapturing(st, &captured) == hipSuccess && captured != hipStreamCaptureStatusNone) {
+    *in_capture = true;
+    if (need == 0) return FC_GGUF_OK;
+    if (!holds(need)) return FC_GGUF_ENOMEM;
+    h->graphed = true;
+    return FC_GGUF_OK;
+  }
+  if (holds(bound)) return FC_GGUF_OK;
   if (fail_workspace()) return FC_GGUF_ENOMEM;
   if (counters < h->counters) counters = h->counters;
   if (counters < 1024) counters = 1024;
-  const size_t total = counter_bytes(counters) + bytes;
-  if (h->ws) {
-    const hipError_t e = hipFreeAsync(h->ws, st);
-    h->ws = nullptr;
-    h->ws_bytes = 0;
-    h->counters = 0;
-    if (e != hipSuccess) return FC_GGUF_EHIP;
-  }
-  if (hipMallocAsync(&h->ws, total, st) != hipSuccess) {
-    h->ws = nullptr;
+  const size_t had = h->ws ? h->ws_bytes - counter_bytes(h->counters) : 0;
+  const size_t total = counter_bytes(counters) + (bound > had ? bound : had);
+  KeptWorkspace* keep = nullptr;
+  if (h->graphed && !(keep = new (std::nothrow) KeptWorkspace)) return FC_GGUF_ENOMEM;
+  void* ws = nullptr;
+  if (hipMallocAsync(&ws, total, st) != hipSuccess) {
+    delete keep;
     return FC_GGUF_ENOMEM;
   }
+  hipError_t e = hipSuccess;
+  if (keep) {
+    *keep = {h->ws, h->kept};
+    h->kept = keep;
+  } else if (h->ws) {
+    e = hipFreeAsync(h->ws, st);
+  }
+  h->ws = ws;
   h->ws_bytes = total;
   h->counters = counters;
   h->fresh = true;
-  return FC_GGUF_OK;
+  h->graphed = false;
+  return e == hipSuccess ? FC_GGUF_OK : FC_GGUF_EHIP;
 }
 
 // a [tokens][heads][D] argument: 16-byte pieces, rows that do not overlap
@@ -128,12 +154,17 @@ int fc_gguf_kv_destroy(fc_gguf_kv_t h) {
   if (!h) return FC_GGUF_OK;
   if (h->ws) {
     // the handle's device, whichever is current: its work must end before the
-    // workspace is freed
+    // workspaces are freed
     int cur = -1;
     const bool switched =
         hipGetDevice(&cur) == hipSuccess && cur != h->device && hipSetDevice(h->device) == hipSuccess;
     (void)hipDeviceSynchronize();                  // best effort: the handle goes anyway
     (void)hipFreeAsync(h->ws, nullptr);
+    while (KeptWorkspace* k = h->kept) {
+      (void)hipFreeAsync(k->p, nullptr);
+      h->kept = k->next;
+      delete k;
+    }
     (void)hipStreamSynchronize(nullptr);
     if (switched) (void)hipSetDevice(cur);
   }
@@ -230,14 +261,18 @@ int fc_gguf_kv_attend(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_hea
       ((int64_t)a.max_q * a.group / 16 + 1) * seqs * h->kv.kv_heads >= ((int64_t)1 << 23))
     return FC_GGUF_ERANGE;
   const fcg::AttendPlan p = fcg::attend_plan(a, h->num_cu);
-  const int rc = ensure_kv_ws(h, seqs * h->kv.kv_heads, fcg::attend_workspace_bytes(a, p), (hipStream_t)stream);
+  const size_t need = fcg::attend_workspace_bytes(a, p), bound = fcg::attend_workspace_bound(a, h->num_cu);
+  bool in_capture;
+  const int rc = ensure_kv_ws(h, seqs * h->kv.kv_heads, need, bound > need ? bound : need, (hipStream_t)stream, &in_capture);
   if (rc != FC_GGUF_OK) return rc;
-  a.arrived = (uint32_t*)h->ws;
-  a.counters = h->counters;
-  a.fresh = h->fresh;
-  a.part = (float*)((char*)h->ws + counter_bytes(h->counters));
+  if (need || (h->fresh && !in_capture)) {
+    a.arrived = (uint32_t*)h->ws;
+    a.counters = h->counters;
+    a.fresh = h->fresh;
+    a.part = (float*)((char*)h->ws + counter_bytes(h->counters));
+  }
   if (fcg::launch_attend(a, p, h->dtype, (hipStream_t)stream) != hipSuccess) return FC_GGUF_EHIP;
-  h->fresh = false;
+  if (!in_capture) h->fresh = false;       // (what is captured has not run yet)
   return FC_GGUF_OK;
 }
 

@@ -301,14 +301,22 @@ typedef struct fc_gguf_kv* fc_gguf_kv_t;
  * kv_heads <= 1024.  The memory need not be initialised.  The handle belongs
  * to the device current now.  It owns a workspace for attention whose keys are
  * dealt to several workgroups, grown stream-ordered as an FC handle's is: one
- * handle must not attend on two streams at once, and a graph is captured after
- * a call of the largest sizes (growth in a captured stream is FC_GGUF_ENOMEM).
+ * handle must not attend on two streams at once.  A call makes the workspace
+ * large enough for every call that is smaller in T, seqs, max_q, table_width
+ * and q_heads (which may need more than the larger one), so a graph is captured
+ * after one call of the largest sizes; growth in a captured stream is
+ * FC_GGUF_ENOMEM.  A workspace that a captured call uses stays as it is until
+ * fc_gguf_kv_destroy, whatever later calls need: a graph may be replayed after
+ * calls of any sizes.  At most about 4/3 * CUs * 256 * (head_dim + 2) * 4 bytes
+ * (45 MB for 256 CUs and 128 dimensions), and as much again for each growth
+ * after a capture.
  */
 int fc_gguf_kv_create(int64_t pages, int page_size, int kv_heads, int head_dim, int dtype, void* k_pages,
                       void* v_pages, fc_gguf_kv_t* out);
 
 /* Frees the handle and its workspace (not the pages); NULL is accepted.
- * Synchronises the handle's device if a workspace was in use. */
+ * Synchronises the handle's device if a workspace was in use.  Graphs that
+ * captured its calls must not be replayed any more. */
 int fc_gguf_kv_destroy(fc_gguf_kv_t h);
 
 /*
