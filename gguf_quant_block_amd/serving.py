@@ -208,6 +208,10 @@ class PagedKv:
         ts, one = table.stride()
         if one != 1 and width > 1:
             raise ValueError("table: contiguous rows")
+        if ts < width:
+            if seqs > 1:
+                raise ValueError("table: rows that do not overlap")
+            ts = width
         if out is None:
             out = torch.zeros((t, heads, dim), dtype=dtype, device=self.device)
         os = _heads(out, heads, dim, dtype, dev, "out")
@@ -218,7 +222,7 @@ class PagedKv:
             _floats(lse, t * heads, dev, "lse")
             lp = lse.data_ptr()
         rc = _call("fc_gguf_kv_attend")(self._h, q.data_ptr(), qs, heads, t, cu_q.data_ptr(), kv_lens.data_ptr(), seqs,
-                                        table.data_ptr(), max(ts, width), width, max_q,
+                                        table.data_ptr(), ts, width, max_q,
                                         self.scale if scale is None else scale, window, out.data_ptr(), os, lp,
                                         _stream(dev))
         if rc != 0:
