@@ -217,6 +217,9 @@ class PagedKv:
         os = _heads(out, heads, dim, dtype, dev, "out")
         if out.shape[0] != t:
             raise ValueError("out: one row for each token")
+        # (the library's call takes 32 and 64 bits of them, and refuses what is out of its range in these)
+        if not (-2**31 <= window < 2**31 and -2**63 <= max_q < 2**63):
+            raise ValueError("window, max_q: out of range")
         lp = None
         if lse is not None:
             _floats(lse, t * heads, dev, "lse")

@@ -39,3 +39,15 @@ def test_rows_of_a_table_must_not_overlap(kv):
     assert kv.calls[-1][1][TABLE_STRIDE:TABLE_WIDTH + 1] == (6, 3)
     kv.attend(q[:1], cu[:2], lens[:1], row[None].expand(1, -1), 1)           # (of one row the stride says nothing)
     assert kv.calls[-1][1][TABLE_STRIDE:TABLE_WIDTH + 1] == (3, 3)
+
+
+def test_windows_past_32_bits_are_refused(kv):
+    q, args = torch.zeros((1, 4, 64), dtype=torch.float16), (_ints(0, 1), _ints(5), _ints(0)[None], 1)
+    for window in (2**31, 2**32 + 5, 2**40, -2**32 + 7):                     # (the call takes 32 bits of them)
+        with pytest.raises(ValueError):
+            kv.attend(q, *args, window=window)
+    with pytest.raises(ValueError):
+        kv.attend(q, *args[:3], 2**64 + 1)
+    assert not kv.calls
+    kv.attend(q, *args, window=2**30)
+    assert len(kv.calls) == 1
