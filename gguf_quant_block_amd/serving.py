@@ -76,6 +76,20 @@ def _floats(x, n, index, name):
         raise ValueError(f"{name}: {n} contiguous float32 values on cuda:{index}")
 
 
+def _overlap(p, ps, pw, q, qs, qw, rows):
+    """Whether rows of pw bytes, ps bytes apart from address p on, share memory with as many of qw bytes, qs apart from q on."""
+    if p + (rows - 1) * ps + pw <= q or q + (rows - 1) * qs + qw <= p or rows == 0:
+        return False
+    if rows == 1:
+        return True
+    if ps < pw or qs < qw:                                # (no rows of the library's: it refuses them)
+        return False
+    if ps == qs:                                          # parts of one matrix's rows, as a rule: rows j and j + k
+        return max((q - p - pw) // ps + 1, 1 - rows) <= min((q - p + qw - 1) // ps, rows - 1)
+    return any(max((at - pw) // ps + 1, 0) <= min((at + qw - 1) // ps, rows - 1)
+               for at in range(q - p, q - p + rows * qs, qs))
+
+
 class Rope:
     """A rotation: inv_freq f32[rot_dim/2] on the GPU, axis i32[rot_dim/2] (the
     position axis that turns each pair) or None, pairs (2j, 2j+1) if
@@ -155,19 +169,25 @@ class PagedKv:
         _ints(slots, dev, "slots", 1)
         if v.shape[0] != t or slots.shape[0] != t:
             raise ValueError("k, v and slots: one row for each token")
+        kp, vp = k.data_ptr(), v.data_ptr()
         qp = op = None
         heads = qs = os = 0
         if q is not None:
             qs = _heads(q, None, dim, dtype, dev, "q")
             rows, heads, _ = q.shape
-            if out is None:
+            given = out is not None
+            if not given:
                 out = torch.empty((t, heads, dim), dtype=dtype, device=self.device)
             os = _heads(out, heads, dim, dtype, dev, "out")
             if rows != t or out.shape[0] != t:
                 raise ValueError("q and out: one row for each token")
             qp, op = q.data_ptr(), out.data_ptr()
-            if qp == op and qs != os:
-                raise ValueError("out: q itself, or other memory")
+            if given:
+                w, kw = 2 * heads * dim, 2 * self.kv_heads * dim
+                if (qp != op or qs != os) and _overlap(op, 2 * os, w, qp, 2 * qs, w, t):
+                    raise ValueError("out: q itself, or other memory")
+                if _overlap(op, 2 * os, w, kp, 2 * ks, kw, t) or _overlap(op, 2 * os, w, vp, 2 * vs, kw, t):
+                    raise ValueError("out: no memory of k or v")
         pp, axes, fp, ap, rot, inter, scale = None, 1, None, None, 0, 0, 1.0
         if rope is not None:
             _need(positions is not None, "positions: needed with a rope")
@@ -181,7 +201,7 @@ class PagedKv:
                 raise ValueError(f"rope: on cuda:{dev}")
             pp, fp, rot, inter, scale = positions.data_ptr(), rope.freq_ptr, rope.rot_dim, rope.interleaved, rope.scale
             ap = rope.axis_ptr
-        rc = _call("fc_gguf_kv_append")(self._h, qp, qs, heads, k.data_ptr(), ks, v.data_ptr(), vs, t, slots.data_ptr(), pp,
+        rc = _call("fc_gguf_kv_append")(self._h, qp, qs, heads, kp, ks, vp, vs, t, slots.data_ptr(), pp,
                                         axes, fp, ap, rot, inter, scale, op, os, _stream(dev))
         if rc != 0:
             _check(rc, "fc_gguf_kv_append")
@@ -212,11 +232,15 @@ class PagedKv:
             if seqs > 1:
                 raise ValueError("table: rows that do not overlap")
             ts = width
-        if out is None:
+        given = out is not None
+        if not given:
             out = torch.zeros((t, heads, dim), dtype=dtype, device=self.device)
         os = _heads(out, heads, dim, dtype, dev, "out")
         if out.shape[0] != t:
             raise ValueError("out: one row for each token")
+        qp, op = q.data_ptr(), out.data_ptr()
+        if given and _overlap(op, 2 * os, 2 * heads * dim, qp, 2 * qs, 2 * heads * dim, t):
+            raise ValueError("out: no memory of q")
         # (the library's call takes 32 and 64 bits of them, and refuses what is out of its range in these)
         if not (-2**31 <= window < 2**31 and -2**63 <= max_q < 2**63):
             raise ValueError("window, max_q: out of range")
@@ -224,10 +248,9 @@ class PagedKv:
         if lse is not None:
             _floats(lse, t * heads, dev, "lse")
             lp = lse.data_ptr()
-        rc = _call("fc_gguf_kv_attend")(self._h, q.data_ptr(), qs, heads, t, cu_q.data_ptr(), kv_lens.data_ptr(), seqs,
+        rc = _call("fc_gguf_kv_attend")(self._h, qp, qs, heads, t, cu_q.data_ptr(), kv_lens.data_ptr(), seqs,
                                         table.data_ptr(), ts, width, max_q,
-                                        self.scale if scale is None else scale, window, out.data_ptr(), os, lp,
-                                        _stream(dev))
+                                        self.scale if scale is None else scale, window, op, os, lp, _stream(dev))
         if rc != 0:
             _check(rc, "fc_gguf_kv_attend")
         return out
@@ -246,7 +269,8 @@ def process_logits(x, *, tokens=None, lens=None, prompt_lens=None, repetition=No
     if dev < 0 or dtype is None or x.dim() != 2:
         raise ValueError("x: f16, bf16 or f32 [rows, vocab] on the GPU")
     rows, vocab = x.shape
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty((rows, vocab), dtype=torch.float32, device=x.device)
     out_dtype = DTYPES.get(out.dtype)
     if out_dtype is None or out.get_device() != dev or out.shape != x.shape:
@@ -257,6 +281,11 @@ def process_logits(x, *, tokens=None, lens=None, prompt_lens=None, repetition=No
         raise ValueError("x and out: contiguous rows")
     if rows <= 1:
         xs, os = max(xs, vocab), max(os, vocab)
+    xp, op = x.data_ptr(), out.data_ptr()
+    if given and (xp != op or xs != os or dtype != out_dtype):
+        size, out_size = 4 if dtype == F32 else 2, 4 if out_dtype == F32 else 2
+        if _overlap(op, out_size * os, out_size * vocab, xp, size * xs, size * vocab, rows):
+            raise ValueError("out: x itself, or other memory")
     tp, ts, lp, pp = None, 0, None, None
     if tokens is not None:
         _ints(tokens, dev, "tokens", 2)
@@ -294,8 +323,8 @@ def process_logits(x, *, tokens=None, lens=None, prompt_lens=None, repetition=No
         mp, ms = mask.data_ptr(), mask.shape[1]
     if torch.cuda.current_device() != dev:
         raise ValueError(f"x: on the current device, not on cuda:{dev}")
-    rc = _call("fc_gguf_logits")(x.data_ptr(), xs, dtype, rows, vocab, tp, ts, lp, pp, rp, fp, sp, bo, bi, bv, bn, mp, ms,
-                                 out.data_ptr(), os, out_dtype, _stream(dev))
+    rc = _call("fc_gguf_logits")(xp, xs, dtype, rows, vocab, tp, ts, lp, pp, rp, fp, sp, bo, bi, bv, bn, mp, ms,
+                                 op, os, out_dtype, _stream(dev))
     if rc != 0:
         _check(rc, "fc_gguf_logits")
     return out

@@ -51,3 +51,67 @@ def test_windows_past_32_bits_are_refused(kv):
     assert not kv.calls
     kv.attend(q, *args, window=2**30)
     assert len(kv.calls) == 1
+
+
+def test_outputs_that_overlap_inputs_are_refused(kv):
+    flat = torch.zeros(4096, dtype=torch.float16)
+    rows = lambda at, stride, heads=4, t=3: flat.as_strided((t, heads, 64), (stride, 64, 1), at)  # noqa: E731
+    cu, lens, table = _ints(0, 3), _ints(5), _ints(0)[None]
+    slots, k, v = _ints(0, 1, 2), torch.zeros((3, 2, 64), dtype=torch.float16), torch.zeros((3, 2, 64), dtype=torch.float16)
+    for q, out, apart in ((rows(0, 256), rows(0, 256), False), (rows(0, 256), rows(256, 256), False), (rows(0, 256), rows(8, 256), False),
+                          (rows(0, 256), rows(768, 256), True), (rows(768, 256), rows(0, 256), True),
+                          (rows(0, 512), rows(256, 512), True), (rows(256, 512), rows(0, 512), True),     # columns of one matrix
+                          (rows(0, 512), rows(248, 512), False), (rows(0, 512), rows(264, 512), False),
+                          (rows(0, 1024), rows(256, 280), False), (rows(0, 1024), rows(256, 256), True),  # rows between its rows
+                          (rows(1032, 1032), rows(0, 520), False),
+                          (rows(0, 512, t=1), rows(256, 512, t=1), True), (rows(0, 512, t=1), rows(8, 512, t=1), False)):
+        t = q.shape[0]
+        kv.calls.clear()
+        same = q.data_ptr() == out.data_ptr()
+        args = (_ints(0, t), lens, table, t)
+        if apart:
+            kv.attend(q, *args, out=out)
+            kv.append(q, k[:t], v[:t], slots[:t], out=out)
+            kv.append(None if t == 3 else q, k[:t], v[:t], slots[:t], out=out)
+            assert len(kv.calls) == 3
+        else:
+            with pytest.raises(ValueError):
+                kv.attend(q, *args, out=out)
+            if same:                                                         # append rotates in place
+                kv.append(q, k[:t], v[:t], slots[:t], out=out)
+            else:
+                with pytest.raises(ValueError):
+                    kv.append(q, k[:t], v[:t], slots[:t], out=out)
+            assert len(kv.calls) == same
+    # keys and values among the output's rows
+    kv.calls.clear()
+    q = torch.zeros((3, 4, 64), dtype=torch.float16)
+    for part in (rows(0, 512, 2), rows(128, 512, 2), rows(392, 512, 2)):
+        for kk, vv in ((part, v), (k, part)):
+            with pytest.raises(ValueError):
+                kv.append(q, kk, vv, slots, out=rows(0, 512))
+    assert not kv.calls
+    qkv = rows(0, 512, 8)
+    kv.append(qkv[:, :4], qkv[:, 4:6], qkv[:, 6:], slots, out=qkv[:, :4])    # one projection's rows, in place
+    assert len(kv.calls) == 1
+
+
+def test_logits_that_overlap_are_refused(monkeypatch):
+    calls = []
+    monkeypatch.setitem(serving._calls, "fc_gguf_logits", lambda *a: calls.append(a) or 0)
+    monkeypatch.setattr(serving, "_stream", lambda index: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    flat = torch.zeros(1000, dtype=torch.float32)
+    half = flat.view(torch.float16)
+    x = flat.as_strided((3, 40), (80, 1))
+    for out in (flat.as_strided((3, 40), (80, 1), 1), flat.as_strided((3, 40), (80, 1), 80), flat.as_strided((3, 40), (40, 1))):
+        with pytest.raises(ValueError):
+            serving.process_logits(x, out=out)
+    with pytest.raises(ValueError):                                          # f16 logits, f32 outputs over them
+        serving.process_logits(half.as_strided((3, 40), (80, 1)), out=flat.as_strided((3, 40), (40, 1)))
+    assert not calls
+    serving.process_logits(x, out=x)
+    serving.process_logits(x, out=flat.as_strided((3, 40), (80, 1), 40))
+    serving.process_logits(x, out=flat.as_strided((3, 40), (40, 1), 240))
+    assert len(calls) == 3
