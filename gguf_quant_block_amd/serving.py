@@ -77,7 +77,8 @@ def _floats(x, n, index, name):
 
 
 def _overlap(p, ps, pw, q, qs, qw, rows):
-    """Whether rows of pw bytes, ps bytes apart from address p on, share memory with as many of qw bytes, qs apart from q on."""
+    """Whether rows of pw bytes, ps bytes apart from address p on, share memory
+    with as many of qw bytes, qs apart from q on."""
     if p + (rows - 1) * ps + pw <= q or q + (rows - 1) * qs + qw <= p or rows == 0:
         return False
     if rows == 1:
@@ -183,10 +184,12 @@ class PagedKv:
                 raise ValueError("q and out: one row for each token")
             qp, op = q.data_ptr(), out.data_ptr()
             if given:
-                w, kw = 2 * heads * dim, 2 * self.kv_heads * dim
-                if (qp != op or qs != os) and _overlap(op, 2 * os, w, qp, 2 * qs, w, t):
+                w, kw, n = 2 * heads * dim, 2 * self.kv_heads * dim, 2 * (t - 1)
+                end = op + n * os + w                     # (most calls end at the comparisons of the whole ranges)
+                if qp < end and op < qp + n * qs + w and (qp != op or qs != os) and _overlap(op, 2 * os, w, qp, 2 * qs, w, t):
                     raise ValueError("out: q itself, or other memory")
-                if _overlap(op, 2 * os, w, kp, 2 * ks, kw, t) or _overlap(op, 2 * os, w, vp, 2 * vs, kw, t):
+                if (kp < end and op < kp + n * ks + kw and _overlap(op, 2 * os, w, kp, 2 * ks, kw, t)
+                        or vp < end and op < vp + n * vs + kw and _overlap(op, 2 * os, w, vp, 2 * vs, kw, t)):
                     raise ValueError("out: no memory of k or v")
         pp, axes, fp, ap, rot, inter, scale = None, 1, None, None, 0, 0, 1.0
         if rope is not None:
@@ -239,7 +242,9 @@ class PagedKv:
         if out.shape[0] != t:
             raise ValueError("out: one row for each token")
         qp, op = q.data_ptr(), out.data_ptr()
-        if given and _overlap(op, 2 * os, 2 * heads * dim, qp, 2 * qs, 2 * heads * dim, t):
+        w = 2 * heads * dim
+        if (given and qp < op + 2 * (t - 1) * os + w and op < qp + 2 * (t - 1) * qs + w
+                and _overlap(op, 2 * os, w, qp, 2 * qs, w, t)):
             raise ValueError("out: no memory of q")
         # (the library's call takes 32 and 64 bits of them, and refuses what is out of its range in these)
         if not (-2**31 <= window < 2**31 and -2**63 <= max_q < 2**63):
