@@ -54,7 +54,8 @@ __device__ __forceinline__ bool find_tile(const AttendArgs& a, int b, int hk, in
   for (int s0 = 0; s0 < a.seqs && s < 0; s0 += 64) {
     RowTile u;                                     // (of this lane's sequence; t is the same in every lane)
     const bool rows = s0 + lane < a.seqs && row_tile(a, s0 + lane, hk, 0, 1, a.stream_rows + 1, INT32_MAX, 1, u);
-    const int n = rows ? (u.rows + tile_rows - 1) / tile_rows : 0;
+    const int each = rows ? (u.rows + tile_rows - 1) / tile_rows : 0;
+    const int n = each < (1 << 24) ? each : 1 << 24;   // (no grid is that large: so that 64 of them add up in 32 bits)
     int sum = n;
 #pragma unroll
     for (int k = 1; k < 64; k *= 2) {
@@ -173,12 +174,6 @@ __device__ __forceinline__ float other_half(float x) {
   asm("" : "+v"(b));                            // (of two equal operands the compiler takes the results for equal too)
   const auto y = __builtin_amdgcn_permlane32_swap(a, b, false, false);   // {own low half twice, own high half twice}
   return __builtin_bit_cast(float, threadIdx.x & 32 ? y[0] : y[1]);
-}
-
-// most tiles of `rows` rows that the sequences of a key head have
-inline int64_t tile_count(const AttendArgs& a, int rows) {
-  const int64_t by_rows = a.T * a.group / rows + a.seqs, each = ((int64_t)a.max_q * a.group + rows - 1) / rows * a.seqs;
-  return by_rows < each ? by_rows : each;
 }
 
 hipError_t launch_attend_tile(const AttendArgs& a, const AttendPlan& p, int dtype, hipStream_t st);

@@ -65,8 +65,8 @@ AttendPlan attend_plan(const AttendArgs& a, int num_cu) {
     // 10 us, a tile of 64 keys 1.5 (600 over 600: 24 us, in two splits 28);
     // of 256 where those would leave half of the CUs idle (twice 11 tokens
     // over 5645 keys of 256 dimensions: 49 us and 36).
-    // The grid has under 2^23 workgroups, those without rows among them.
-    const int64_t room = ((int64_t)1 << 23) / (tile_count(a, p.tile_rows) * hk);
+    // The grid holds them all, those without rows among them.
+    const int64_t room = (kMaxWorkgroups - 1) / (tile_count(a, p.tile_rows) * hk);
     int64_t want = (num_cu + tiles / 2) / tiles;
     if (want > room) want = room;
     const int64_t few = tiles * ((span(p.tile_rows, 64) + 767) / 768) < num_cu / 2;

@@ -86,6 +86,7 @@ constexpr int at_stream_rows(int D) { return D == 256 ? 16 : 32; }   // at most 
 constexpr int AT_TILE = 32;
 constexpr int at_waves(int D) { return D == 256 ? 4 : 8; }
 constexpr int at_step(int D) { return at_waves(D) * AT_TILE; }
+constexpr int64_t kMaxWorkgroups = (int64_t)1 << 23;   // of 512 threads: fewer than these
 struct AttendPlan {
   int stream_rows;            // most rows of a streamed sequence
   int splits;                 // shares of the streaming kernel
@@ -97,6 +98,12 @@ AttendPlan attend_plan(const AttendArgs& a, int num_cu);
 size_t attend_part_rows(const AttendArgs& a, const AttendPlan& p);
 size_t attend_workspace_bytes(const AttendArgs& a, const AttendPlan& p);
 hipError_t launch_attend(const AttendArgs& a, const AttendPlan& p, int dtype, hipStream_t st);
+
+// most tiles of `rows` rows that the sequences of a key head have
+inline int64_t tile_count(const AttendArgs& a, int rows) {
+  const int64_t by_rows = a.T * a.group / rows + a.seqs, each = ((int64_t)a.max_q * a.group + rows - 1) / rows * a.seqs;
+  return by_rows < each ? by_rows : each;
+}
 
 // A bound of attend_workspace_bytes over this call and all that are smaller in
 // T, seqs, max_q, table width and heads, whatever their windows: a workspace

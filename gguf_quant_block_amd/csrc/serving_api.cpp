@@ -256,9 +256,10 @@ int fc_gguf_kv_attend(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_hea
   a.max_q = (int)(max_q < T ? max_q : T);
   a.window = window;
   a.scale_log2 = scale_log2;
-  // a launch has under 2^32 threads
-  if ((int64_t)a.max_q * a.group > kMaxTokens ||
-      ((int64_t)a.max_q * a.group / 16 + 1) * seqs * h->kv.kv_heads >= ((int64_t)1 << 23))
+  // A launch has under 2^32 threads: 512 for each tile of at least 128 rows
+  // that T tokens of seqs sequences can have, and for each sequence that is not
+  // split.  (The splits and their join are launched for few tiles only.)
+  if ((int64_t)a.max_q * a.group > kMaxTokens || fcg::tile_count(a, 128) * h->kv.kv_heads >= fcg::kMaxWorkgroups)
     return FC_GGUF_ERANGE;
   const fcg::AttendPlan p = fcg::attend_plan(a, h->num_cu);
   const size_t need = fcg::attend_workspace_bytes(a, p), bound = fcg::attend_workspace_bound(a, h->num_cu);

@@ -374,9 +374,11 @@ int fc_gguf_kv_append(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_hea
  * by T, max_q and table_width, which the host knows; lengths are read on the
  * device, so a captured graph may be replayed with other lengths within them.
  * The order of summation depends on sizes and lengths only: equal calls give
- * equal bits.  seqs <= 65535;
- * table_width * page_size and window <= 2^30; (min(max_q, T) * q_heads /
- * kv_heads / 16 + 1) * seqs * kv_heads < 2^23; T, seqs or max_q == 0 is a no-op.
+ * equal bits.  Limits (else FC_GGUF_ERANGE): T, max_q, window and table_width *
+ * page_size <= 2^30, seqs <= 65535, and, with g = q_heads / kv_heads,
+ * m = min(max_q, T): m * g <= 2^30 and kv_heads times the smaller of
+ * T * g / 128 + seqs and (m * g / 128, rounded up) * seqs under 2^23.  T, seqs
+ * or max_q == 0 is a no-op.
  */
 int fc_gguf_kv_attend(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_heads, int64_t T,
                       const int32_t* cu_q, const int32_t* kv_lens, int64_t seqs, const int32_t* table,
