@@ -25,7 +25,7 @@
 //
 // Bound by the matrix and vector instructions of a wave's 32 rows, and by the
 // clock that the card holds under them: 4096 tokens over 8192 keys (32 heads
-// of 128 on 8 key heads, f16) take 396 to 421 us on different cards, 980 to
+// of 128 on 8 key heads, f16) take 398 to 431 us on different cards, 960 to
 // 1040 TFLOP/s, where a product of two 8192 x 8192 matrices reaches 1200; the
 // matrix cores are busy for 397 of 798 thousand cycles, at about 2 GHz.  4
 // waves of 64 rows spilled (454 TFLOP/s).  The weights are rounded to the

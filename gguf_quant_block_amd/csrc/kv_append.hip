@@ -10,8 +10,9 @@
 // taken once per token and pair into LDS and serve every head.  The rotation
 // is in f32 with one rounding to the cache's type.  Measured: 4096 tokens, 32
 // query and 8 key heads of 128: 22.3 us, 4.5 TB/s (a copy reaches 4.75; HBM
-// writes 1.11 of the bytes, for cache lines that several workgroups fill);
-// 2500 tokens on three axes 16.6 us; one token 4.9 us, most of it the launch.
+// writes 1.11 of the bytes, for cache lines that several workgroups fill), 29.6
+// where nothing is cached; 2500 tokens on three axes 16.2 us, and 24.2; one
+// token 5.3 us, most of it the launch.
 //
 // A workgroup takes tokens_per_wg consecutive tokens (1 for a decode step,
 // where latency counts and the heads are spread over y_splits workgroups; up

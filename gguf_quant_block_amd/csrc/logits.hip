@@ -12,12 +12,12 @@
 //
 // A workgroup takes a slice of one row's tokens.  It counts the row's history
 // in LDS (whole numbers, so that the order of the atomics changes nothing) and
-// puts the row's biases beside them, then passes over its logits once, 16
-// bytes of the narrower type at a time.  Its logits are read before the
-// history, so that only one of the two waits is paid.  Entries of a bias list
-// that name the same token are added in the list's order: one wave takes 64
-// entries at a time, and each lane first sums its token's entries among them
-// in order.
+// puts the row's biases beside them, then passes over its logits once, four
+// values at a time (16 bytes of f32, 8 of f16 and bf16).  Its logits are read
+// before the history, so that only one of the two waits is paid.  Entries of a
+// bias list that name the same token are added in the list's order: one wave
+// takes 64 entries at a time, and each lane first sums its token's entries among
+// them in order.
 #include <math.h>
 
 #include "serving.h"

@@ -1,7 +1,7 @@
 // C-ABI of the serving operators (declarations and contracts in
 // include/fc_gguf.h): the paged key/value cache, attention over it and the
-// processing of logits.  Host logic only: argument checks, the split of the
-// keys and the workspace of the split sums.
+// processing of logits.  Host logic only: argument checks and the workspace of
+// the split sums.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -180,7 +180,6 @@ int fc_gguf_kv_append(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_hea
   if (!h || T < 0 || q_heads < 0) return FC_GGUF_EINVAL;
   if (const int rc = check_kv_device(h); rc != FC_GGUF_OK) return rc;
   const int D = h->kv.head_dim, hk = h->kv.kv_heads;
-  // (a launch has under 2^32 threads)
   // (a launch has under 2^32 threads: 512 for 8 tokens)
   if (q_heads > 65536 || T > ((int64_t)1 << 25)) return FC_GGUF_ERANGE;
   if (inv_freq) {

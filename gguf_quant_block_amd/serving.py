@@ -115,7 +115,8 @@ class PagedKv:
     k [pages, kv_heads, head_dim/8, page_size, 8] and v [pages, kv_heads,
     page_size/8, head_dim, 8], f16 or bf16 on the GPU, are allocated here
     (uninitialised) unless given.  They may be read, and whole pages copied in
-    and out, like any tensors.
+    and out, like any tensors.  A graph that captures attend is captured after
+    one call of its largest sizes, and must not outlive the cache.
     """
 
     def __init__(self, pages, page_size, kv_heads, head_dim, dtype=torch.float16, *, device=None, k=None, v=None):

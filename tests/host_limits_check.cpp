@@ -1,7 +1,8 @@
 // Host check of which sizes of an attention call are taken, without a GPU: the
 // plan is the library's own.  Every call that is taken must launch grids of
 // under 2^32 threads and tiles that the kernels can count in 32 bits; steps of
-// a long chunk beside hundreds of single tokens must be taken.  Prints "ok" and
+// a long chunk beside hundreds of single tokens must be taken.  An append takes
+// 2^25 tokens and no more.  Prints "ok" and
 // returns 0, or the first line that does not hold.
 #include <stdio.h>
 #include <random>
@@ -62,6 +63,17 @@ int main() {
     }
     fc_gguf_kv_destroy(kv);
   }
+  // tokens of an append: 2^25
+  if (fc_gguf_kv_create(100000, 64, 2, 64, 0, mem, mem, &kv)) return 1;
+  for (int64_t over : {0, 1}) {
+    const int rc = fc_gguf_kv_append(kv, nullptr, 0, 0, mem, 128, mem, 128, ((int64_t)1 << 25) + over, i, nullptr, 1, nullptr, nullptr, 0, 0,
+                                     1.f, nullptr, 0, nullptr);
+    if (rc != (over ? FC_GGUF_ERANGE : 0)) {
+      printf("2^25 + %ld tokens: code %d\n", (long)over, rc);
+      return 1;
+    }
+  }
+  fc_gguf_kv_destroy(kv);
   std::mt19937_64 g(1);
   auto up_to = [&](int64_t n) { return (int64_t)std::exp(std::uniform_real_distribution<>(0, std::log((double)n + .99))(g)); };
   const int dims[] = {64, 96, 128, 256};
