@@ -527,20 +527,15 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
 template <class E, int D>
 hipError_t join_launch(const AttendArgs& a, hipStream_t st) {
   if (a.splits == 1) return hipSuccess;
-  attend_join_kernel<E, D><<<dim3((unsigned)(tile_count(a, join_rows(D)) * a.kv.kv_heads)), 256, 0, st>>>(a);
-  return hipGetLastError();
+  return launch_kernel(attend_join_kernel<E, D>, dim3((unsigned)(tile_count(a, join_rows(D)) * a.kv.kv_heads)), 256, 0, st, a);
 }
 
 template <class E, int D>
 hipError_t stream_d(const AttendArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)(a.shares * a.kv.kv_heads));
   if constexpr (D < 256)
-    if (a.stream_rows > 16) {
-      attend_stream_kernel<E, D, 2><<<grid, at_waves(D) * 64, 0, st>>>(a);
-      return hipGetLastError();
-    }
-  attend_stream_kernel<E, D, 1><<<grid, at_waves(D) * 64, 0, st>>>(a);
-  return hipGetLastError();
+    if (a.stream_rows > 16) return launch_kernel(attend_stream_kernel<E, D, 2>, grid, at_waves(D) * 64, 0, st, a);
+  return launch_kernel(attend_stream_kernel<E, D, 1>, grid, at_waves(D) * 64, 0, st, a);
 }
 
 template <class E>
@@ -553,8 +548,8 @@ hipError_t launch_e(const AttendArgs& a, bool join, hipStream_t st) {
   }
 }
 
-__global__ __launch_bounds__(256) void zero_kernel(uint32_t* p, int64_t n) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
+__global__ __launch_bounds__(256) void zero_kernel(AttendArgs a) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.counters; i += (int64_t)gridDim.x * 256) a.arrived[i] = 0;
 }
 
 }  // namespace
@@ -567,8 +562,7 @@ hipError_t launch_attend(const AttendArgs& args, const AttendPlan& p, int dtype,
   a.whole = p.whole;
   if (a.fresh) {
     const int64_t wgs = (a.counters + 255) / 256;
-    zero_kernel<<<dim3((unsigned)(wgs < 1024 ? wgs : 1024)), 256, 0, st>>>(a.arrived, a.counters);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = launch_kernel(zero_kernel, dim3((unsigned)(wgs < 1024 ? wgs : 1024)), 256, 0, st, a);
     if (e != hipSuccess) return e;
   }
   if (p.tile_rows) {

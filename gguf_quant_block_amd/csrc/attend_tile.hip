@@ -412,8 +412,7 @@ hipError_t tile_launch(const AttendArgs& a, hipStream_t st) {
   const hipError_t e = raise_lds_limit((const void*)attend_tile_kernel<E, D, WAVES, BIG>, C::LDS, raised);
   if (e != hipSuccess) return e;
   const int64_t wgs = tile_count(a, C::ROWS) * a.splits * a.kv.kv_heads;
-  attend_tile_kernel<E, D, WAVES, BIG><<<dim3((unsigned)wgs), WAVES * 64, C::LDS, st>>>(a);
-  return hipGetLastError();
+  return launch_kernel(attend_tile_kernel<E, D, WAVES, BIG>, dim3((unsigned)wgs), WAVES * 64, C::LDS, st, a);
 }
 
 template <class E, int D, int WAVES>

@@ -201,12 +201,11 @@ __global__ __launch_bounds__(AP_THREADS) void kv_append_kernel(AppendArgs a) {
 template <class E, int THREADS>
 hipError_t append_e(const AppendArgs& a, dim3 grid, hipStream_t st) {
   switch (a.kv.head_dim) {
-    case 64: kv_append_kernel<E, 64, THREADS><<<grid, THREADS, 0, st>>>(a); break;
-    case 96: kv_append_kernel<E, 96, THREADS><<<grid, THREADS, 0, st>>>(a); break;
-    case 128: kv_append_kernel<E, 128, THREADS><<<grid, THREADS, 0, st>>>(a); break;
-    default: kv_append_kernel<E, 256, THREADS><<<grid, THREADS, 0, st>>>(a);
+    case 64: return launch_kernel(kv_append_kernel<E, 64, THREADS>, grid, THREADS, 0, st, a);
+    case 96: return launch_kernel(kv_append_kernel<E, 96, THREADS>, grid, THREADS, 0, st, a);
+    case 128: return launch_kernel(kv_append_kernel<E, 128, THREADS>, grid, THREADS, 0, st, a);
+    default: return launch_kernel(kv_append_kernel<E, 256, THREADS>, grid, THREADS, 0, st, a);
   }
-  return hipGetLastError();
 }
 
 }  // namespace

@@ -148,9 +148,9 @@ hipError_t launch_io(const LogitsArgs& a, int num_cu, hipStream_t st) {
   // row of 32064: 11 us and 4; 128 rows of 131073 f32 in slices of 4096, 512
   // threads: 27.9 us, 256 threads: 33.9, slices of 8192: 35.6, of 2048: 29.1).
   const int64_t wide = (a.vocab + 4095) / 4096, narrow = (a.vocab + 1023) / 1024;
-  if (wide * a.rows >= 2 * num_cu) logits_kernel<I, O, 512, 4, 2><<<dim3((unsigned)wide, (unsigned)a.rows), 512, 0, st>>>(a);
-  else logits_kernel<I, O, 256, 4, 1><<<dim3((unsigned)narrow, (unsigned)a.rows), 256, 0, st>>>(a);
-  return hipGetLastError();
+  if (wide * a.rows >= 2 * num_cu)
+    return launch_kernel(logits_kernel<I, O, 512, 4, 2>, dim3((unsigned)wide, (unsigned)a.rows), 512, 0, st, a);
+  return launch_kernel(logits_kernel<I, O, 256, 4, 1>, dim3((unsigned)narrow, (unsigned)a.rows), 256, 0, st, a);
 }
 
 }  // namespace

@@ -35,6 +35,18 @@ struct KvPages {
   int head_dim;
 };
 
+// Launches kernel(args) and returns this launch's own status, which is then not
+// left behind as well.  (After <<<>>> there is only the thread's last error,
+// which an earlier call of anyone may have left: the launch would be reported
+// as failed.)
+template <class Args>
+hipError_t launch_kernel(void (*kernel)(Args), dim3 grid, int threads, size_t lds, hipStream_t st, const Args& args) {
+  void* p[] = {const_cast<Args*>(&args)};
+  const hipError_t e = hipLaunchKernel((const void*)kernel, grid, dim3(threads), p, lds, st);
+  if (e != hipSuccess) (void)hipGetLastError();
+  return e;
+}
+
 struct AppendArgs {
   KvPages kv;
   const uint16_t* q;   // [T][q_heads][D], row strides in elements

@@ -93,6 +93,7 @@ int ensure_kv_ws(fc_gguf_kv* h, int64_t counters, size_t need, size_t bound, hip
   if (h->graphed && !(keep = new (std::nothrow) KeptWorkspace)) return FC_GGUF_ENOMEM;
   void* ws = nullptr;
   if (hipMallocAsync(&ws, total, st) != hipSuccess) {
+    (void)hipGetLastError();     // (reported by the code: not left behind as well)
     delete keep;
     return FC_GGUF_ENOMEM;
   }
