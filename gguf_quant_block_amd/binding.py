@@ -49,10 +49,15 @@ _SIGS = {
     # the serving operators (serving.py)
     "fc_gguf_kv_create": (ctypes.c_int, [_c_i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _vp,
                                          ctypes.POINTER(_vp)]),
+    "fc_gguf_kv_create8": (ctypes.c_int, [_c_i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp,
+                                          _vp, ctypes.POINTER(_vp)]),
     "fc_gguf_kv_destroy": (ctypes.c_int, [_vp]),
     "fc_gguf_kv_append": (ctypes.c_int, [_vp, _vp, _c_i64, ctypes.c_int, _vp, _c_i64, _vp, _c_i64, _c_i64, _vp, _vp,
                                          ctypes.c_int, _vp, _vp, ctypes.c_int, ctypes.c_int, ctypes.c_float, _vp,
                                          _c_i64, _vp]),
+    "fc_gguf_kv_append_norm": (ctypes.c_int, [_vp, _vp, _c_i64, ctypes.c_int, _vp, _c_i64, _vp, _c_i64, _c_i64, _vp, _vp,
+                                              _c_i64, _vp, _c_i64, ctypes.c_float, _vp, ctypes.c_int, _vp, _vp,
+                                              ctypes.c_int, ctypes.c_int, ctypes.c_float, _vp, _c_i64, _vp]),
     "fc_gguf_kv_attend": (ctypes.c_int, [_vp, _vp, _c_i64, ctypes.c_int, _c_i64, _vp, _vp, _c_i64, _vp, _c_i64,
                                          _c_i64, _c_i64, ctypes.c_float, ctypes.c_int, _vp, _c_i64, _vp, _vp]),
     "fc_gguf_logits": (ctypes.c_int, [_vp, _c_i64, ctypes.c_int, _c_i64, _c_i64, _vp, _c_i64, _vp, _vp, _vp, _vp, _vp,

@@ -110,6 +110,49 @@ __device__ __forceinline__ float reference_of(float mx, float scale_log2) {
 // and NaN against 1 for a key that the row sees; 64 keys at most, so that the
 // sum is exact and says how many there are of each.
 
+// ---- the cache of 8 bits ----
+
+// the scales of 8 keys' values, from their stored exponents
+template <class E> struct ValueScales;
+template <> struct ValueScales<f16> {            // in pairs, as factors of f16 values
+  u32x4 by;
+  __device__ __forceinline__ ValueScales(uint2 e) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t w = (j < 2 ? e.x : e.y) >> (16 * (j & 1));
+      by[j] = (held_exponent<f16>(w & 0xFFu) - 112u) << 10 | (held_exponent<f16>(w >> 8 & 0xFFu) - 112u) << 26;
+    }
+  }
+  // 8 codes of a dimension as values: exact, a power of two times what is in range
+  __device__ __forceinline__ u32x4 values(uint32_t lo, uint32_t hi) const {
+    u32x4 v = codes8<f16>(lo, hi, 1.f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t x = v[j], y = by[j];          // (an element itself is not taken by a bit cast: it gives the first)
+      v[j] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, x) * __builtin_bit_cast(half2v, y));
+    }
+    return v;
+  }
+};
+template <> struct ValueScales<bf16> {
+  float by[8];
+  __device__ __forceinline__ ValueScales(uint2 e) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) by[j] = __builtin_bit_cast(float, held_exponent<bf16>((j < 4 ? e.x : e.y) >> (8 * (j & 3)) & 0xFFu) << 23);
+  }
+  __device__ __forceinline__ u32x4 values(uint32_t lo, uint32_t hi) const {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    u32x4 v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t w = j < 2 ? lo : hi;
+      const f32x2 y = j & 1 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true) : __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+      v[j] = pack2<bf16>(y.x * by[2 * j], y.y * by[2 * j + 1]);
+    }
+    return v;
+  }
+};
+
 // all ones over the first n of a piece's 8 keys
 __device__ __forceinline__ u32x4 keep_keys(int n) {
   u32x4 k;

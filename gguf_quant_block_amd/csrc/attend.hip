@@ -40,18 +40,30 @@ namespace fcg {
 namespace {
 
 // Keys [c0, c1) of a sequence's rows: the sums and statistics of this wave.
-template <class E, int D, int RT>
+//
+// Q8: a cache of 8 bits.  A 16-byte load is then two pieces, the same 8
+// dimensions of keys 2r and 2r + 1 of the tile for lane row r, or the same 8
+// keys of dimensions 2r and 2r + 1 of 32.  One of the two goes to each of a pair
+// of operands, so that row r of half h of the first product is key 2r + h, and
+// of the second dimension 32 (d / 2) + 2r + d % 2.  A lane still ends with the
+// scores of keys 8g .. 8g + 7, in another order.  Codes become values of E
+// where they are used, exactly (serving.h): what follows is the same.
+template <class E, int D, int RT, bool Q8>
 struct Piece {
   static constexpr int KS = D / 32, DT = D / 16, AT_STEP = at_step(D);
+  // where the score of the lane's key j stands: half, and element of it
+  static constexpr int half_of(int j) { return Q8 ? j & 1 : j >> 2; }
+  static constexpr int row_of(int j) { return Q8 ? j >> 1 : j & 3; }
   floatx4 o[RT][DT];
   float m[RT], l[RT];
 
   __device__ __forceinline__ void run(const AttendArgs& a, const RowTile& t, int c0, int c1) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
     const int ps = 1 << a.kv.page_shift, hk = t.hk;
-    const int64_t page_bytes = (int64_t)a.kv.kv_heads * ps * D * 2;
-    const uint8_t* kbase = (const uint8_t*)a.kv.k + (int64_t)hk * ps * D * 2;
-    const uint8_t* vbase = (const uint8_t*)a.kv.v + (int64_t)hk * ps * D * 2;
+    constexpr int B = Q8 ? 1 : 2;                // bytes of an element
+    const int64_t page_bytes = (int64_t)a.kv.kv_heads * ps * D * B;
+    const uint8_t* kbase = (const uint8_t*)a.kv.k + (int64_t)hk * ps * D * B;
+    const uint8_t* vbase = (const uint8_t*)a.kv.v + (int64_t)hk * ps * D * B;
     const int32_t* table = a.table + t.s * a.table_stride;
 
     // The page of the 16 keys that hold a lane's key rows (r / 8) and of those
@@ -60,25 +72,40 @@ struct Piece {
     // Entries of the table are read a step before they are looked at.
     auto entry_at = [&](int key) -> int { return table[(key < c1 ? key : c1 - 1) >> a.kv.page_shift]; };
     auto page_of = [&](int key, int entry) -> int { return key < c1 && (unsigned)entry < (uint64_t)a.kv.pages ? entry : -1; };
-    u32x4 kr[2][KS], vr[DT];
+    constexpr int KH = Q8 ? 1 : 2, VT = Q8 ? DT / 2 : DT;
+    u32x4 kr[KH][KS], vr[VT];
+    uint32_t ke = 0;                               // Q8: the stored exponents of the lane's two keys,
+    uint2 ve = {0, 0};                             // and of the 8 whose values it has
+    auto scales_at = [&](const uint8_t* scales, int page, int key) -> const uint8_t* {
+      return scales + ((int64_t)(page < 0 ? 0 : page) * a.kv.kv_heads + hk) * ps + (key & (ps - 1));
+    };
     // key of row r of half h of a tile: 8 (r / 4) + 4 h + r % 4
     auto load_k = [&](int tok0, int page) {
       const uint8_t* p = kbase + (page < 0 ? 0 : page) * page_bytes;
+      if constexpr (Q8) {
+        const int key = tok0 + 2 * r;
+        ke = *(const uint16_t*)scales_at(a.kv.k_scale, page, key);
+        const uint8_t* x = p + ((key & (ps - 1)) + g * ps) * 8;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int key = tok0 + 8 * (r >> 2) + 4 * h + (r & 3);
-        const uint8_t* x = p + ((key & (ps - 1)) + g * ps) * 16;
+        for (int k = 0; k < KS; ++k) kr[0][k] = *(const u32x4*)(x + k * 4 * ps * 8);
+      } else {
 #pragma unroll
-        for (int k = 0; k < KS; ++k) kr[h][k] = *(const u32x4*)(x + k * 4 * ps * 16);
+        for (int h = 0; h < KH; ++h) {
+          const int key = tok0 + 8 * (r >> 2) + 4 * h + (r & 3);
+          const uint8_t* x = p + ((key & (ps - 1)) + g * ps) * 16;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) kr[h][k] = *(const u32x4*)(x + k * 4 * ps * 16);
+        }
       }
     };
     auto v_at = [&](int tok0, int page) -> const uint8_t* {
-      return vbase + (page < 0 ? 0 : page) * page_bytes + ((((tok0 + 8 * g) & (ps - 1)) >> 3) * D + r) * 16;
+      return vbase + (page < 0 ? 0 : page) * page_bytes + ((((tok0 + 8 * g) & (ps - 1)) >> 3) * D + (Q8 ? 2 * r : r)) * 8 * B;
     };
     auto load_v = [&](int tok0, int page) {
       const uint8_t* p = v_at(tok0, page);
+      if constexpr (Q8) ve = *(const uint2*)scales_at(a.kv.v_scale, page, tok0 + 8 * g);
 #pragma unroll
-      for (int d = 0; d < DT; ++d) vr[d] = *(const u32x4*)(p + d * 256);
+      for (int d = 0; d < VT; ++d) vr[d] = *(const u32x4*)(p + d * 256);
     };
     // every row sees every key of the tile: no mask
     auto is_open = [&](int tok0, int page) {
@@ -125,26 +152,49 @@ struct Piece {
     for (; tok0 < c1; tok0 += AT_STEP) {
       const int next = tok0 + AT_STEP;
       floatx4 sc[RT][2];
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
+      if constexpr (Q8) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          floatx4 c = {0.f, 0.f, 0.f, 0.f};
+          const float by = __builtin_bit_cast(float, held_exponent<E>(ke >> (8 * h) & 0xFFu) << 23);
 #pragma unroll
-          for (int k = 0; k < KS; ++k) c = Mat<E>::mfma16(kr[h][k], q[i][k], c);
-          sc[i][h] = c;
+          for (int i = 0; i < RT; ++i) sc[i][h] = (floatx4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            const u32x4 x = codes8<E>(kr[0][k][2 * h], kr[0][k][2 * h + 1], by);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) sc[i][h] = Mat<E>::mfma16(x, q[i][k], sc[i][h]);
+          }
         }
+      } else {
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            floatx4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < KS; ++k) c = Mat<E>::mfma16(kr[h][k], q[i][k], c);
+            sc[i][h] = c;
+          }
+      }
       // (past the last tile the loads are of the pool's first page, for nothing)
       load_k(next, page_of(next + ko, ek));
       ek = entry_at(next + AT_STEP + ko);
 
+      u32x4 decoded[Q8 ? DT : 1];
+      auto pick = [&]() -> auto& { if constexpr (Q8) return decoded; else return vr; };
+      auto& vals = pick();                         // the tile's values
+      if constexpr (Q8) {
+        const ValueScales<E> scales(ve);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) vals[d] = scales.values(vr[d / 2][2 * (d & 1)], vr[d / 2][2 * (d & 1) + 1]);
+      }
       if (!is_open(tok0, pv)) {
         const int key0 = tok0 + 8 * g, n = have(tok0, pv);
         const u32x4 keep = keep_keys(n);
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          vr[d] &= keep;                           // stale values must not meet a weight of 0 as NaN
-          bad |= take_nonfinite<E>(vr[d]);
+          vals[d] &= keep;                         // stale values must not meet a weight of 0 as NaN
+          bad |= take_nonfinite<E>(vals[d]);
         }
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
@@ -152,7 +202,7 @@ struct Piece {
           const int low = a.window > 0 ? pos[i] - a.window - key0 : -1;    // last before its window
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (j > top || j <= low) sc[i][j >> 2][j & 3] = -INFINITY;
+            if (j > top || j <= low) sc[i][half_of(j)][row_of(j)] = -INFINITY;
         }
       }
 
@@ -170,7 +220,7 @@ struct Piece {
         float p[8], sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          p[j] = __builtin_amdgcn_exp2f(fmaf(sc[i][j >> 2][j & 3], a.scale_log2, -ms));
+          p[j] = __builtin_amdgcn_exp2f(fmaf(sc[i][half_of(j)][row_of(j)], a.scale_log2, -ms));
           sum += p[j];
         }
         l[i] = l[i] * al + sum;
@@ -180,7 +230,7 @@ struct Piece {
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           o[i][d] *= al;
-          o[i][d] = Mat<E>::mfma16(vr[d], w, o[i][d]);
+          o[i][d] = Mat<E>::mfma16(vals[d], w, o[i][d]);
         }
       }
       pv = page_of(next + vo, ev);
@@ -194,13 +244,21 @@ struct Piece {
         if (is_open(tok0, page)) continue;
         const int key0 = tok0 + 8 * g, n = have(tok0, page);
         const uint8_t* p = v_at(tok0, page);
+        auto values_of = [&](int d) -> u32x4 {
+          if constexpr (Q8) {
+            const u32x4 x = *(const u32x4*)(p + (d / 2) * 256);
+            return ValueScales<E>(*(const uint2*)scales_at(a.kv.v_scale, page, key0)).values(x[2 * (d & 1)], x[2 * (d & 1) + 1]);
+          } else {
+            return *(const u32x4*)(p + d * 256);
+          }
+        };
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
           const u32x4 one = seen_ones<E>(pos[i] - key0 < n ? pos[i] - key0 : n - 1, a.window > 0 ? pos[i] - a.window - key0 : -1);
 #pragma unroll
           for (int d = 0; d < DT; ++d) {
             floatx4 c = {0.f, 0.f, 0.f, 0.f};
-            c = Mat<E>::mfma16(nonfinite_codes<E>(*(const u32x4*)(p + d * 256) & keep_keys(n)), one, c);
+            c = Mat<E>::mfma16(nonfinite_codes<E>(values_of(d) & keep_keys(n)), one, c);
 #pragma unroll
             for (int x = 0; x < 4; ++x) o[i][d][x] += nonfinite_sum(c[x]);
           }
@@ -322,7 +380,7 @@ __device__ __forceinline__ void join_pieces(const AttendArgs& a, int q0, int row
 // workgroup has two at most, the end of a sequence (or its middle; slot 0) and
 // the beginning of one (slot 1).  They go to the workspace, and the workgroup
 // that brings a sequence's last piece joins them.
-template <class E, int D, int RT>
+template <class E, int D, int RT, bool Q8>
 __global__ __launch_bounds__(at_waves(D) * 64, at_waves(D) / 4) void attend_stream_kernel(AttendArgs a) {
   constexpr int DT = D / 16, AT_WAVES = at_waves(D), AT_STEP = at_step(D);
   constexpr int PITCH = D + 4;                    // floats of a row in LDS
@@ -384,7 +442,7 @@ __global__ __launch_bounds__(at_waves(D) * 64, at_waves(D) / 4) void attend_stre
     const int off = (int)(at - g0), take = (int)(to - at < n - off ? to - at : n - off);
     const bool whole = take == n;
     const int c0 = t.beg + off * AT_STEP, c1 = off + take == n ? t.end : c0 + take * AT_STEP;
-    Piece<E, D, RT> p;
+    Piece<E, D, RT, Q8> p;
     p.run(a, t, c0, c1);
 
     // join the waves
@@ -399,8 +457,16 @@ __global__ __launch_bounds__(at_waves(D) * 64, at_waves(D) / 4) void attend_stre
     for (int i = 0; i < RT; ++i) {
       __syncthreads();
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
-        *(floatx4*)&sums[(wave * 16 + r) * PITCH + d * 16 + g * 4] = p.o[i][d];
+      for (int d = 0; d < DT; ++d) {
+        float* to = &sums[(wave * 16 + r) * PITCH];
+        if constexpr (Q8) {                        // dimensions 8g .. of 32, from two operands in turn
+          const floatx4 x = p.o[i][d & ~1], y = p.o[i][d | 1];
+          const int e = 2 * (d & 1);
+          *(floatx4*)&to[d / 2 * 32 + g * 8 + 2 * e] = (floatx4){x[e], y[e], x[e + 1], y[e + 1]};
+        } else {
+          *(floatx4*)&to[d * 16 + g * 4] = p.o[i][d];
+        }
+      }
       __syncthreads();
       for (int y0 = tid; y0 < 16 * (D / 8); y0 += AT_WAVES * 64) {
         const int rr = y0 / (D / 8), d0 = (y0 - rr * (D / 8)) * 8, row = i * 16 + rr;
@@ -530,12 +596,17 @@ hipError_t join_launch(const AttendArgs& a, hipStream_t st) {
   return launch_kernel(attend_join_kernel<E, D>, dim3((unsigned)(tile_count(a, join_rows(D)) * a.kv.kv_heads)), 256, 0, st, a);
 }
 
-template <class E, int D>
-hipError_t stream_d(const AttendArgs& a, hipStream_t st) {
+template <class E, int D, bool Q8>
+hipError_t stream_q(const AttendArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)(a.shares * a.kv.kv_heads));
   if constexpr (D < 256)
-    if (a.stream_rows > 16) return launch_kernel(attend_stream_kernel<E, D, 2>, grid, at_waves(D) * 64, 0, st, a);
-  return launch_kernel(attend_stream_kernel<E, D, 1>, grid, at_waves(D) * 64, 0, st, a);
+    if (a.stream_rows > 16) return launch_kernel(attend_stream_kernel<E, D, 2, Q8>, grid, at_waves(D) * 64, 0, st, a);
+  return launch_kernel(attend_stream_kernel<E, D, 1, Q8>, grid, at_waves(D) * 64, 0, st, a);
+}
+
+template <class E, int D>
+hipError_t stream_d(const AttendArgs& a, hipStream_t st) {
+  return a.kv.k_scale ? stream_q<E, D, true>(a, st) : stream_q<E, D, false>(a, st);
 }
 
 template <class E>

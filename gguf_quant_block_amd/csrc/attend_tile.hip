@@ -34,6 +34,8 @@
 // are f32, the totals of the unrounded weights.
 #include <math.h>
 
+#include <type_traits>
+
 #include "attend.h"
 
 namespace fcg {
@@ -70,7 +72,9 @@ __device__ __forceinline__ void barrier_if(bool on) {
 
 // BIG: pages of KT keys or more, so that a tile is in one page and where it
 // begins is the same in every lane.
-template <class E, int D, int WAVES, bool BIG>
+// Q8: a cache of 8 bits.  Its codes become values of E on their way to LDS, once
+// for all waves (exactly: serving.h), and nothing after that knows of them.
+template <class E, int D, int WAVES, bool BIG, bool Q8>
 __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kernel(AttendArgs a) {
   using C = TileCfg<D, WAVES>;
   static_assert(D / 8 % WAVES == 0, "pieces per wave");
@@ -90,9 +94,11 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
   split_range(t, split, a.splits, a.per_split, c0, c1);
 
   const int ps = 1 << a.kv.page_shift;
-  const int64_t page_bytes = (int64_t)a.kv.kv_heads * ps * D * 2;
-  const uint8_t* kbase = (const uint8_t*)a.kv.k + (int64_t)hk * ps * D * 2;
-  const uint8_t* vbase = (const uint8_t*)a.kv.v + (int64_t)hk * ps * D * 2;
+  constexpr int B = Q8 ? 1 : 2;                  // bytes of an element
+  typedef typename std::conditional<Q8, uint2, u32x4>::type Raw;   // a piece in memory
+  const int64_t page_bytes = (int64_t)a.kv.kv_heads * ps * D * B;
+  const uint8_t* kbase = (const uint8_t*)a.kv.k + (int64_t)hk * ps * D * B;
+  const uint8_t* vbase = (const uint8_t*)a.kv.v + (int64_t)hk * ps * D * B;
   const int32_t* table = a.table + t.s * a.table_stride;
 
   // rows of this wave
@@ -135,32 +141,45 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
     return page < 0 ? 0 : (c1 - tok0 < KT ? ((uint64_t)1 << (c1 - tok0)) - 1 : ~0ull);
   };
   // pieces of keys and of values on their way to LDS
-  u32x4 kst[NI], vst[NI];
+  Raw kraw[NI], vraw[NI];
+  u32x4 vst[NI];
+  // Q8: the stored exponents of the lane's key, and of the 8 keys of each piece of values
+  uint32_t ke = 0;
+  uint2 ve[NI];
+  // where the scales of a page that begins `start` bytes into the pool begin: a byte for D
+  auto scales_at = [&](const uint8_t* scales, uint64_t start, int key) -> const uint8_t* {
+    return scales + start / D + (uint32_t)(hk * ps + (key & (ps - 1)));
+  };
   auto load_k = [&](int tok0, uint64_t start) {
     if constexpr (BIG) {
-      const uint8_t* kp = kbase + start + (uint32_t)((tok0 & (ps - 1)) * 16 + wave * NI * ps * 16);
+      const uint8_t* kp = kbase + start + (uint32_t)((tok0 & (ps - 1)) * 8 * B + wave * NI * ps * 8 * B);
 #pragma unroll
-      for (int i = 0; i < NI; ++i) kst[i] = *(const u32x4*)(kp + (uint32_t)(i * ps * 16) + (uint32_t)lane * 16);
+      for (int i = 0; i < NI; ++i) kraw[i] = *(const Raw*)(kp + (uint32_t)(i * ps * 8 * B) + (uint32_t)lane * 8 * B);
     } else {
-      const uint8_t* kp = kbase + start + (((tok0 + lane) & (ps - 1)) * 16 + wave * NI * ps * 16);
+      const uint8_t* kp = kbase + start + (((tok0 + lane) & (ps - 1)) * 8 * B + wave * NI * ps * 8 * B);
 #pragma unroll
-      for (int i = 0; i < NI; ++i) kst[i] = *(const u32x4*)(kp + (uint32_t)(i * ps * 16));
+      for (int i = 0; i < NI; ++i) kraw[i] = *(const Raw*)(kp + (uint32_t)(i * ps * 8 * B));
     }
+    if constexpr (Q8) ke = *scales_at(a.kv.k_scale, start, tok0 + lane);
   };
   auto load_v = [&](int tok0, uint64_t start) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       if constexpr (BIG) {                       // pieces of a page follow each other
-        vst[i] = *(const u32x4*)(vbase + start + (uint32_t)((tok0 & (ps - 1)) * (D * 2) + (wave * NI + i) * 1024) + (uint32_t)lane * 16);
+        vraw[i] = *(const Raw*)(vbase + start + (uint32_t)((tok0 & (ps - 1)) * (D * B) + (wave * NI + i) * 512 * B) + (uint32_t)lane * 8 * B);
+        if constexpr (Q8) ve[i] = *(const uint2*)scales_at(a.kv.v_scale, start, tok0 + ((wave * NI + i) * 64 + (D % 64 ? lane : 0)) / D * 8);
       } else if constexpr (D % 64 == 0) {        // the wave's 64 pieces are of the same 8 keys
         const int p = (wave * NI + i) * 64, k8 = p / D, d = p - k8 * D;
         const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(start >> 32), k8 * 8) << 32 |
                             (uint32_t)__builtin_amdgcn_readlane((int)start, k8 * 8);
-        const uint8_t* vp = vbase + at + (uint32_t)(((tok0 + k8 * 8) & (ps - 1)) * (D * 2) + d * 16);
-        vst[i] = *(const u32x4*)(vp + (uint32_t)lane * 16);
+        const uint8_t* vp = vbase + at + (uint32_t)(((tok0 + k8 * 8) & (ps - 1)) * (D * B) + d * 8 * B);
+        vraw[i] = *(const Raw*)(vp + (uint32_t)lane * 8 * B);
+        if constexpr (Q8) ve[i] = *(const uint2*)scales_at(a.kv.v_scale, at, tok0 + k8 * 8);
       } else {
         const int p = (wave * NI + i) * 64 + lane, k8 = p / D, d = p - k8 * D;
-        vst[i] = *(const u32x4*)(vbase + __shfl(start, k8 * 8) + (uint32_t)(((tok0 + k8 * 8) & (ps - 1)) * (D * 2) + d * 16));
+        const uint64_t at = __shfl(start, k8 * 8);
+        vraw[i] = *(const Raw*)(vbase + at + (uint32_t)(((tok0 + k8 * 8) & (ps - 1)) * (D * B) + d * 8 * B));
+        if constexpr (Q8) ve[i] = *(const uint2*)scales_at(a.kv.v_scale, at, tok0 + k8 * 8);
       }
     }
   };
@@ -168,9 +187,24 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
   if (tid == 0) *flag = 0;
   __syncthreads();
   uint8_t* const mine = smem + (wave * NI * 64 + lane) * 16;
-  auto store = [&](int at, const u32x4* x) {     // at: where the tile's pieces begin
+  auto store_v = [&](int at) {                   // at: where the tile's pieces begin
 #pragma unroll
-    for (int i = 0; i < NI; ++i) *(u32x4*)(mine + at + i * 1024) = x[i];
+    for (int i = 0; i < NI; ++i) *(u32x4*)(mine + at + i * 1024) = vst[i];
+  };
+  auto store_k = [&](int at) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      if constexpr (Q8) {
+        const float by = __builtin_bit_cast(float, held_exponent<E>(ke) << 23);
+        *(u32x4*)(mine + at + i * 1024) = codes8<E>(kraw[i].x, kraw[i].y, by);
+      } else {
+        *(u32x4*)(mine + at + i * 1024) = kraw[i];
+      }
+    }
+  };
+  auto piece_of = [&](const Raw& x, const uint2& e) -> u32x4 {   // of values
+    if constexpr (Q8) return ValueScales<E>(e).values(x.x, x.y);
+    else return x;
   };
   // the key of operand row r, in pieces
   const int krow = ((r >> 4) & 1) * 16 + ((r >> 2) & 1) * 8 + ((r >> 3) & 1) * 4 + (r & 3);
@@ -190,6 +224,8 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
   // A masked key's weight is 0, which must not meet an infinite or NaN value:
   // of tiles with masked keys those are stored as 0 and added at the end.
   auto clean = [&](int tok0, uint64_t ok) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) vst[i] = piece_of(vraw[i], ve[i]);
     if (is_open(tok0, ok, t.lo, t.hi)) return;
     if (ok != ~0ull)
 #pragma unroll
@@ -285,12 +321,12 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
     int e3 = entry_at(c0 + 3 * KT);
     uint64_t ok = paged(c0, p0), ok1 = paged(c0 + KT, p1), ok2 = paged(c0 + 2 * KT, p2), start2 = start_of(p2);
     load_k(c0, start_of(p0));
-    store(C::KB, kst);
+    store_k(C::KB);
     load_v(c0, start_of(p0));
     load_k(c0 + KT, start_of(p1));
     clean(c0, ok);
-    store(C::STAGE, vst);
-    store(C::STAGE + C::KB, kst);
+    store_v(C::STAGE);
+    store_k(C::STAGE + C::KB);
     load_v(c0 + KT, start_of(p1));
     load_k(c0 + 2 * KT, start2);
     half_barrier();
@@ -304,8 +340,8 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
       weights(tok0, ok);
       __builtin_amdgcn_sched_barrier(0);
       clean(tok0 + KT, ok1);
-      store(next, vst);
-      store(next + C::KB, kst);
+      store_v(next);
+      store_k(next + C::KB);
       half_barrier();
       // (past the last tile the loads are of keys without a page, never read)
       load_v(tok0 + 2 * KT, start2);
@@ -347,8 +383,11 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
           const int key0 = tok0 + s * 16 + 8 * h, n = have(tok0, ok, 2 * s + h);
           const u32x4 one = seen_ones<E>(pos - key0 < n ? pos - key0 : n - 1, a.window > 0 ? pos - a.window - key0 : -1);
           const int pg = BIG ? page : __shfl(page, s * 16 + 8 * h);
-          const u32x4 v = *(const u32x4*)(vbase + start_of(pg) +
-                                          ((((in_page + s * 16 + 8 * h) & (ps - 1)) >> 3) * D + d * 32 + r) * 16);
+          const Raw x = *(const Raw*)(vbase + start_of(pg) +
+                                      ((((in_page + s * 16 + 8 * h) & (ps - 1)) >> 3) * D + d * 32 + r) * 8 * B);
+          uint2 e = {0, 0};
+          if constexpr (Q8) e = *(const uint2*)scales_at(a.kv.v_scale, start_of(pg), key0);
+          const u32x4 v = piece_of(x, e);
           c = Mat<E>::mfma32(nonfinite_codes<E>(v & keep_keys(n)), one, c);
         }
 #pragma unroll
@@ -405,19 +444,21 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
   }
 }
 
-template <class E, int D, int WAVES, bool BIG>
+template <class E, int D, int WAVES, bool BIG, bool Q8>
 hipError_t tile_launch(const AttendArgs& a, hipStream_t st) {
   using C = TileCfg<D, WAVES>;
   static std::atomic<uint64_t> raised{0};
-  const hipError_t e = raise_lds_limit((const void*)attend_tile_kernel<E, D, WAVES, BIG>, C::LDS, raised);
+  const hipError_t e = raise_lds_limit((const void*)attend_tile_kernel<E, D, WAVES, BIG, Q8>, C::LDS, raised);
   if (e != hipSuccess) return e;
   const int64_t wgs = tile_count(a, C::ROWS) * a.splits * a.kv.kv_heads;
-  return launch_kernel(attend_tile_kernel<E, D, WAVES, BIG>, dim3((unsigned)wgs), WAVES * 64, C::LDS, st, a);
+  return launch_kernel(attend_tile_kernel<E, D, WAVES, BIG, Q8>, dim3((unsigned)wgs), WAVES * 64, C::LDS, st, a);
 }
 
 template <class E, int D, int WAVES>
 hipError_t tile_w(const AttendArgs& a, hipStream_t st) {
-  return (1 << a.kv.page_shift) >= KT ? tile_launch<E, D, WAVES, true>(a, st) : tile_launch<E, D, WAVES, false>(a, st);
+  const bool big = (1 << a.kv.page_shift) >= KT;
+  if (a.kv.k_scale) return big ? tile_launch<E, D, WAVES, true, true>(a, st) : tile_launch<E, D, WAVES, false, true>(a, st);
+  return big ? tile_launch<E, D, WAVES, true, false>(a, st) : tile_launch<E, D, WAVES, false, false>(a, st);
 }
 
 template <class E, int D>

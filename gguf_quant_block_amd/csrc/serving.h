@@ -26,9 +26,14 @@ constexpr int DT_F32 = 2;
 // (K) and 8 tokens of one head dimension (V): the two shapes in which the
 // matrix instructions' operands hold 8 consecutive values of the summed index
 // in one lane, for K.Q^T (summed over dimensions) and V^T.P^T (over tokens).
+// In 8 bits the shapes are the same with e4m3 codes as elements, pieces of 8
+// bytes, and each token and key head has two scales, [kv_heads][ps] bytes of a
+// page: the exponents of powers of two, biased by 127.
 struct KvPages {
   void* k;
   void* v;
+  uint8_t* k_scale;    // null: 16 bits
+  uint8_t* v_scale;
   int64_t pages;
   int page_shift;      // log2(tokens per page), 4 .. 8
   int kv_heads;
@@ -61,6 +66,10 @@ struct AppendArgs {
   int64_t T;
   int q_heads, rot, axes, interleaved;
   float rope_scale;
+  const float* q_norm;        // [D], or [heads][D] with stride D; null: none
+  const float* k_norm;
+  int q_norm_stride, k_norm_stride;   // from head to head: 0 or D
+  float eps;
   int tokens_per_wg, y_splits;
 };
 hipError_t launch_kv_append(const AppendArgs& a, int dtype, int num_cu, hipStream_t st);
@@ -198,6 +207,55 @@ template <> struct Mat<bf16> {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
   }
 };
+
+// ---- the cache of 8 bits ----
+//
+// A head of a token is e4m3 codes times 2^e, e = ceil(log2(amax / 448)): a
+// power of two costs a code with an exponent of its own no precision, unlike
+// amax / 448 itself, and what the codes stand for is exact in E.  So that it is
+// finite and exact for every code, e is held to [LO, HI] and codes at HI to 240
+// (448 otherwise): the smallest code, 2^-9, at LO is 2^-23 in f16, where a
+// normal value of the head keeps its three bits down to 2^-20.
+template <class E> struct Held;
+template <> struct Held<f16> { static constexpr int LO = 127 - 14, HI = 127 + 8; };
+template <> struct Held<bf16> { static constexpr int LO = 127 - 110, HI = 127 + 120; };
+constexpr float CODE_MOST = 448.f, CODE_MOST_HI = 240.f;
+constexpr uint32_t CODE_NAN = 0x7F;
+
+// a stored exponent as one that append writes: what stale memory holds is taken
+// as the nearest, so that no scale is infinite
+template <class E>
+__device__ __forceinline__ uint32_t held_exponent(uint32_t b) {
+  const uint32_t x = b < (uint32_t)Held<E>::LO ? (uint32_t)Held<E>::LO : b;
+  return x < (uint32_t)Held<E>::HI ? x : (uint32_t)Held<E>::HI;
+}
+// the stored exponent of a largest magnitude: 448 = 1.75 * 2^8, and a fraction
+// above .75 carries into the exponent
+template <class E>
+__device__ __forceinline__ int exponent_of(float amax) {
+  const int e = (int)((__builtin_bit_cast(uint32_t, amax) + 0x1FFFFFu) >> 23) - 8;
+  return e < Held<E>::LO ? Held<E>::LO : (e < Held<E>::HI ? e : Held<E>::HI);
+}
+
+// Four codes of a dword as E, times the power of two `scale`.
+template <class E> __device__ __forceinline__ void codes4(uint32_t w, float scale, uint32_t& a, uint32_t& b);
+template <>
+__device__ __forceinline__ void codes4<f16>(uint32_t w, float scale, uint32_t& a, uint32_t& b) {
+  a = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, scale, false));
+  b = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, scale, true));
+}
+template <>
+__device__ __forceinline__ void codes4<bf16>(uint32_t w, float scale, uint32_t& a, uint32_t& b) {
+  a = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false));
+  b = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true));
+}
+template <class E>
+__device__ __forceinline__ u32x4 codes8(uint32_t lo, uint32_t hi, float scale) {
+  uint32_t a, b, c, d;
+  codes4<E>(lo, scale, a, b);
+  codes4<E>(hi, scale, c, d);
+  return (u32x4){a, b, c, d};
+}
 
 // two f32 -> two E in a dword, round to nearest even
 template <class E>

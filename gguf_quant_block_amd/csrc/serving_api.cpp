@@ -117,12 +117,8 @@ bool rows_ok(const void* p, int64_t stride, int64_t width) {
   return p && on(p, 16) && stride >= width && stride % 8 == 0;
 }
 
-}  // namespace
-
-extern "C" {
-
-int fc_gguf_kv_create(int64_t pages, int page_size, int kv_heads, int head_dim, int dtype, void* k_pages,
-                      void* v_pages, fc_gguf_kv_t* out) {
+int create_kv(int64_t pages, int page_size, int kv_heads, int head_dim, int dtype, void* k_pages, void* v_pages,
+              uint8_t* k_scales, uint8_t* v_scales, fc_gguf_kv_t* out) {
   if (!out) return FC_GGUF_EINVAL;
   *out = nullptr;
   if (pages <= 0 || kv_heads <= 0 || !k_pages || !v_pages || !on(k_pages, 16) || !on(v_pages, 16))
@@ -135,6 +131,8 @@ int fc_gguf_kv_create(int64_t pages, int page_size, int kv_heads, int head_dim, 
   if (!h) return FC_GGUF_ENOMEM;
   h->kv.k = k_pages;
   h->kv.v = v_pages;
+  h->kv.k_scale = k_scales;
+  h->kv.v_scale = v_scales;
   h->kv.pages = pages;
   h->kv.page_shift = __builtin_ctz((unsigned)page_size);
   h->kv.kv_heads = kv_heads;
@@ -149,6 +147,27 @@ int fc_gguf_kv_create(int64_t pages, int page_size, int kv_heads, int head_dim, 
   }
   *out = h;
   return FC_GGUF_OK;
+}
+
+// weights of a norm: [D], or a row of D for each head
+bool norm_ok(const float* w, int64_t stride, int D) {
+  return !w || (on(w, 16) && (stride == 0 || stride == D));
+}
+
+}  // namespace
+
+extern "C" {
+
+int fc_gguf_kv_create(int64_t pages, int page_size, int kv_heads, int head_dim, int dtype, void* k_pages,
+                      void* v_pages, fc_gguf_kv_t* out) {
+  return create_kv(pages, page_size, kv_heads, head_dim, dtype, k_pages, v_pages, nullptr, nullptr, out);
+}
+
+int fc_gguf_kv_create8(int64_t pages, int page_size, int kv_heads, int head_dim, int dtype, void* k_pages,
+                       void* v_pages, void* k_scales, void* v_scales, fc_gguf_kv_t* out) {
+  if (out) *out = nullptr;
+  if (!k_scales || !v_scales || !on(k_scales, 16) || !on(v_scales, 16)) return FC_GGUF_EINVAL;
+  return create_kv(pages, page_size, kv_heads, head_dim, dtype, k_pages, v_pages, (uint8_t*)k_scales, (uint8_t*)v_scales, out);
 }
 
 int fc_gguf_kv_destroy(fc_gguf_kv_t h) {
@@ -178,6 +197,17 @@ int fc_gguf_kv_append(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_hea
                       const int32_t* positions, int axes, const float* inv_freq, const int32_t* pair_axis,
                       int rot_dim, int interleaved, float rope_scale, void* q_out, int64_t q_out_stride,
                       void* stream) {
+  return fc_gguf_kv_append_norm(h, q, q_stride, q_heads, k, k_stride, v, v_stride, T, slots, nullptr, 0, nullptr, 0, 0.f,
+                                positions, axes, inv_freq, pair_axis, rot_dim, interleaved, rope_scale, q_out,
+                                q_out_stride, stream);
+}
+
+int fc_gguf_kv_append_norm(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_heads, const void* k,
+                           int64_t k_stride, const void* v, int64_t v_stride, int64_t T, const int32_t* slots,
+                           const float* q_norm, int64_t q_norm_stride, const float* k_norm, int64_t k_norm_stride,
+                           float eps, const int32_t* positions, int axes, const float* inv_freq,
+                           const int32_t* pair_axis, int rot_dim, int interleaved, float rope_scale, void* q_out,
+                           int64_t q_out_stride, void* stream) {
   if (!h || T < 0 || q_heads < 0) return FC_GGUF_EINVAL;
   if (const int rc = check_kv_device(h); rc != FC_GGUF_OK) return rc;
   const int D = h->kv.head_dim, hk = h->kv.kv_heads;
@@ -189,6 +219,8 @@ int fc_gguf_kv_append(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_hea
       return FC_GGUF_EINVAL;
     if (axes > 16) return FC_GGUF_ERANGE;
   }
+  if (!norm_ok(q_norm, q_norm_stride, D) || !norm_ok(k_norm, k_norm_stride, D)) return FC_GGUF_EINVAL;
+  if ((q_norm || k_norm) && !(eps >= 0.f && isfinite(eps))) return FC_GGUF_EINVAL;
   if (T == 0) return FC_GGUF_OK;
   if (inv_freq && (!positions || !on(positions, 4))) return FC_GGUF_EINVAL;
   if (!slots || !on(slots, 4) || !rows_ok(k, k_stride, (int64_t)hk * D) || !rows_ok(v, v_stride, (int64_t)hk * D))
@@ -215,6 +247,11 @@ int fc_gguf_kv_append(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_hea
   a.axes = axes;
   a.interleaved = interleaved;
   a.rope_scale = rope_scale;
+  a.q_norm = q_norm;
+  a.k_norm = k_norm;
+  a.q_norm_stride = (int)q_norm_stride;
+  a.k_norm_stride = (int)k_norm_stride;
+  a.eps = eps;
   return fcg::launch_kv_append(a, h->dtype, h->num_cu, (hipStream_t)stream) == hipSuccess ? FC_GGUF_OK
                                                                                          : FC_GGUF_EHIP;
 }

@@ -109,6 +109,33 @@ class Rope:
         self.interleaved, self.scale = bool(interleaved), float(scale)
 
 
+class HeadNorm:
+    """Norms of queries and keys for each head, ahead of the rotation: x / sqrt(mean(x^2) + eps) * weight.  q and k:
+    weights f32 [head_dim], or [heads, head_dim] with a row for each query or key head, on the GPU; None: no norm of
+    these."""
+
+    def __init__(self, q=None, k=None, eps=1e-6):
+        _need(q is not None or k is not None, "q or k: weights of one of the two at least")
+        self.index = (k if q is None else q).get_device()
+        _need(self.index >= 0, "q and k: tensors on the GPU")
+        for w, name in ((q, "q"), (k, "k")):
+            if w is not None:
+                _floats(w, w.numel(), self.index, name)
+                _need(w.dim() in (1, 2) and w.numel() > 0, f"{name}: [head_dim] or [heads, head_dim]")
+        self.q, self.k, self.eps = q, k, float(eps)      # kept alive for their addresses
+        self.q_shape, self.k_shape = (None if w is None else tuple(w.shape) for w in (q, k))
+        self.q_ptr, self.k_ptr = (None if w is None else w.data_ptr() for w in (q, k))
+
+
+def _norm_stride(shape, heads, dim, name):
+    """From head to head of a norm's weights."""
+    if shape == (dim,):
+        return 0
+    if shape != (heads, dim):
+        raise ValueError(f"norm: weights of {name} [{dim}] or [{heads}, {dim}], got {shape}")
+    return dim
+
+
 class PagedKv:
     """One layer's paged key/value cache.
 
@@ -117,19 +144,40 @@ class PagedKv:
     (uninitialised) unless given.  They may be read, and whole pages copied in
     and out, like any tensors.  A graph that captures attend is captured after
     one call of its largest sizes, and must not outlive the cache.
+
+    bits=8: k and v are float8_e4m3fn, and k_scale and v_scale [pages, kv_heads,
+    page_size], float8_e8m0fnu, hold a power of two for each token and head; a
+    page is its rows of all four.  Code times scale is a value of dtype, exactly.
+    append quantises, attend computes with these values; queries, keys, values
+    and outputs are of dtype either way.
     """
 
-    def __init__(self, pages, page_size, kv_heads, head_dim, dtype=torch.float16, *, device=None, k=None, v=None):
-        if k is None or v is None:
-            _need(k is None and v is None, "k and v: both or neither")
+    bits, k_scale, v_scale = 16, None, None
+
+    def __init__(self, pages, page_size, kv_heads, head_dim, dtype=torch.float16, *, device=None, k=None, v=None, bits=16,
+                 k_scale=None, v_scale=None):
+        _need(bits in (8, 16), "bits: 8 or 16")
+        given = [x is not None for x in ((k, v, k_scale, v_scale) if bits == 8 else (k, v))]
+        _need(bits == 8 or (k_scale is None and v_scale is None), "k_scale and v_scale: of 8 bits only")
+        held = dtype if bits == 16 else torch.float8_e4m3fn
+        if not all(given):
+            _need(not any(given), "k and v (and their scales): all or none")
             _need(min(pages, page_size, kv_heads, head_dim) > 0 and head_dim % 8 == 0 and page_size % 8 == 0,
                   "pages, page_size, kv_heads, head_dim: positive, the sizes multiples of 8")
             if not torch.cuda.is_available():
                 raise RuntimeError("no GPU visible: the library has no CPU path")
             device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-            k = torch.empty((pages, kv_heads, head_dim // 8, page_size, 8), dtype=dtype, device=device)
-            v = torch.empty((pages, kv_heads, page_size // 8, head_dim, 8), dtype=dtype, device=device)
-        _need(k.is_cuda and v.is_cuda and k.device == v.device and k.dtype == v.dtype == dtype, "k and v: of dtype, on one GPU")
+            k = torch.empty((pages, kv_heads, head_dim // 8, page_size, 8), dtype=held, device=device)
+            v = torch.empty((pages, kv_heads, page_size // 8, head_dim, 8), dtype=held, device=device)
+            if bits == 8:
+                k_scale, v_scale = (torch.empty((pages, kv_heads, page_size), dtype=torch.float8_e8m0fnu, device=device)
+                                    for _ in range(2))
+        _need(k.is_cuda and v.is_cuda and k.device == v.device and k.dtype == v.dtype == held, f"k and v: of {held}, on one GPU")
+        if bits == 8:
+            _need(all(x.device == k.device and x.dtype == torch.float8_e8m0fnu and x.is_contiguous()
+                      and tuple(x.shape) == (pages, kv_heads, page_size) for x in (k_scale, v_scale)),
+                  "k_scale and v_scale: contiguous float8_e8m0fnu [pages, kv_heads, page_size] beside k and v")
+            self.bits, self.k_scale, self.v_scale = 8, k_scale, v_scale
         _need(k.is_contiguous() and v.is_contiguous() and tuple(k.shape) == (pages, kv_heads, head_dim // 8, page_size, 8)
               and tuple(v.shape) == (pages, kv_heads, page_size // 8, head_dim, 8), "k and v: contiguous, of the cache's shapes")
         self.k, self.v = k, v
@@ -138,9 +186,13 @@ class PagedKv:
         self.scale = 1.0 / math.sqrt(head_dim)
         self._h = ctypes.c_void_p()
         h = ctypes.c_void_p()
+        what = (pages, page_size, kv_heads, head_dim, DTYPES.get(dtype, -1), k.data_ptr(), v.data_ptr())
         with torch.cuda.device(self.device):
-            _check(_call("fc_gguf_kv_create")(pages, page_size, kv_heads, head_dim, DTYPES.get(dtype, -1), k.data_ptr(),
-                                              v.data_ptr(), ctypes.byref(h)), "fc_gguf_kv_create")
+            if bits == 8:
+                _check(_call("fc_gguf_kv_create8")(*what, k_scale.data_ptr(), v_scale.data_ptr(), ctypes.byref(h)),
+                       "fc_gguf_kv_create8")
+            else:
+                _check(_call("fc_gguf_kv_create")(*what, ctypes.byref(h)), "fc_gguf_kv_create")
         self._h = h
 
     @property
@@ -158,11 +210,11 @@ class PagedKv:
         except Exception:
             pass
 
-    def append(self, q, k, v, slots, positions=None, rope=None, out=None):
-        """Rotates q [T, heads, head_dim] and k [T, kv_heads, head_dim] by rope at
+    def append(self, q, k, v, slots, positions=None, rope=None, out=None, norm=None):
+        """Normalises (norm: a HeadNorm) and rotates q [T, heads, head_dim] and k [T, kv_heads, head_dim] by rope at
         positions i32 [T] or [axes, T] (None: no rotation) and appends k and v at
         slots i32 [T] (page * page_size + place; negative: not appended).  Returns
-        the rotated q, in out (q itself, or None for a new tensor).  q may be None:
+        the q so treated, in out (q itself, or None for a new tensor).  q may be None:
         keys and values only.  The three may be parts of one projection's rows."""
         dev, dim, dtype = self.index, self.head_dim, self.dtype
         t = k.shape[0]
@@ -205,8 +257,17 @@ class PagedKv:
                 raise ValueError(f"rope: on cuda:{dev}")
             pp, fp, rot, inter, scale = positions.data_ptr(), rope.freq_ptr, rope.rot_dim, rope.interleaved, rope.scale
             ap = rope.axis_ptr
-        rc = _call("fc_gguf_kv_append")(self._h, qp, qs, heads, kp, ks, vp, vs, t, slots.data_ptr(), pp,
-                                        axes, fp, ap, rot, inter, scale, op, os, _stream(dev))
+        if norm is None:
+            rc = _call("fc_gguf_kv_append")(self._h, qp, qs, heads, kp, ks, vp, vs, t, slots.data_ptr(), pp,
+                                            axes, fp, ap, rot, inter, scale, op, os, _stream(dev))
+        else:
+            if norm.index != dev:
+                raise ValueError(f"norm: on cuda:{dev}")
+            qn, kn = norm.q_ptr if q is not None else None, norm.k_ptr
+            qns = 0 if qn is None else _norm_stride(norm.q_shape, heads, dim, "q")
+            kns = 0 if kn is None else _norm_stride(norm.k_shape, self.kv_heads, dim, "k")
+            rc = _call("fc_gguf_kv_append_norm")(self._h, qp, qs, heads, kp, ks, vp, vs, t, slots.data_ptr(), qn, qns, kn,
+                                                 kns, norm.eps, pp, axes, fp, ap, rot, inter, scale, op, os, _stream(dev))
         if rc != 0:
             _check(rc, "fc_gguf_kv_append")
         return out

@@ -314,6 +314,28 @@ typedef struct fc_gguf_kv* fc_gguf_kv_t;
 int fc_gguf_kv_create(int64_t pages, int page_size, int kv_heads, int head_dim, int dtype, void* k_pages,
                       void* v_pages, fc_gguf_kv_t* out);
 
+/*
+ * A handle over a cache of 8 bits: as fc_gguf_kv_create, and every call on the
+ * handle takes queries, keys, values and outputs of `dtype`, but the elements of
+ * the pages are e4m3 codes of one byte (no infinities, NaN 0x7F and 0xFF) in the
+ * same shapes, and each token and key head has a scale, a power of two:
+ *   k_scales, v_scales  device u8[pages][kv_heads][page_size], 16-byte aligned:
+ *                       the exponents, biased by 127
+ * Append stores, of a head's values x (keys normalised and rotated, from f32),
+ *   amax  the largest magnitude among the finite ones
+ *   e     log2(amax / 448) rounded up, but at least -14 and at most 8 (f16), -110
+ *         and 120 (bf16)
+ *   code  x / 2^e rounded to the nearest (ties to even), magnitudes past 448 (240
+ *         where e is 8 or 120) taken as that; infinite and NaN: NaN
+ * so that code * 2^e is a finite value that dtype holds exactly, or NaN.  Attend
+ * computes with these values, as it would over a 16-bit cache that held them.
+ * (Append stores no exponent outside the two bounds, which would be read as the
+ * nearer one, and no code past 240 at the upper, which is infinite in dtype.)
+ * What masked places hold, stale codes and scales too, changes nothing.
+ */
+int fc_gguf_kv_create8(int64_t pages, int page_size, int kv_heads, int head_dim, int dtype, void* k_pages,
+                       void* v_pages, void* k_scales, void* v_scales, fc_gguf_kv_t* out);
+
 /* Frees the handle and its workspace (not the pages); NULL is accepted.
  * Synchronises the handle's device if a workspace was in use.  Graphs that
  * captured its calls must not be replayed any more. */
@@ -350,6 +372,23 @@ int fc_gguf_kv_append(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_hea
                       void* stream);
 
 /*
+ * fc_gguf_kv_append with norms of queries and keys for each head ahead of the
+ * rotation:
+ *   x = x / sqrt(mean of x^2 over the head + eps) * weight
+ * in f32, and one rounding after the rotation.
+ *   q_norm, k_norm  device f32 [head_dim] (stride 0), or [q_heads | kv_heads]
+ *                   [head_dim] (stride head_dim), 16-byte aligned, or NULL: no
+ *                   norm of these (both NULL: fc_gguf_kv_append)
+ *   eps             finite and >= 0 (not read without norms)
+ */
+int fc_gguf_kv_append_norm(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_heads, const void* k,
+                           int64_t k_stride, const void* v, int64_t v_stride, int64_t T, const int32_t* slots,
+                           const float* q_norm, int64_t q_norm_stride, const float* k_norm, int64_t k_norm_stride,
+                           float eps, const int32_t* positions, int axes, const float* inv_freq,
+                           const int32_t* pair_axis, int rot_dim, int interleaved, float rope_scale, void* q_out,
+                           int64_t q_out_stride, void* stream);
+
+/*
  * Attention of new tokens over the cache: one token per sequence, a chunk of
  * a prompt, or both in one call.
  *   q, out       device [T][q_heads][head_dim] of the cache's type, 16-byte
@@ -373,6 +412,8 @@ int fc_gguf_kv_append(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_hea
  * hold (infinities and NaN included) changes nothing.  The launches are sized
  * by T, max_q and table_width, which the host knows; lengths are read on the
  * device, so a captured graph may be replayed with other lengths within them.
+ * Sums are f32, of weights up to 2^12 with bf16: keys' values past 2^100 may
+ * make them infinite.
  * The order of summation depends on sizes and lengths only: equal calls give
  * equal bits.  Limits (else FC_GGUF_ERANGE): T, max_q, window and table_width *
  * page_size <= 2^30, seqs <= 65535, and, with g = q_heads / kv_heads,
