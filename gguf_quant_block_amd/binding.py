@@ -62,6 +62,9 @@ _SIGS = {
                                          _c_i64, _c_i64, ctypes.c_float, ctypes.c_int, _vp, _c_i64, _vp, _vp]),
     "fc_gguf_logits": (ctypes.c_int, [_vp, _c_i64, ctypes.c_int, _c_i64, _c_i64, _vp, _c_i64, _vp, _vp, _vp, _vp, _vp,
                                       _vp, _vp, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, ctypes.c_int, _vp]),
+    "fc_gguf_sample_workspace": (_c_i64, [_c_i64, _c_i64]),
+    "fc_gguf_sample": (ctypes.c_int, [_vp, _c_i64, ctypes.c_int, _c_i64, _c_i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                      _c_i64, _vp]),
     "fc_gguf_strerror": (ctypes.c_char_p, [ctypes.c_int]),
 }
 

@@ -34,7 +34,7 @@ CFLAGS = [
 ]
 SOURCES = ["fc_gguf_api.cpp", "layout.hip", "gemv.hip", "prefill.hip", "skinny.hip", "prefill_i8.hip",
            "moe.hip", "dequant.hip", "serving_api.cpp", "attend_plan.cpp", "kv_append.hip", "attend.hip", "attend_tile.hip",
-           "logits.hip"]
+           "logits.hip", "sample_api.cpp", "sample.hip"]
 CEIL_SOURCES = ["ceilings.hip"]
 
 

@@ -25,6 +25,17 @@ inline hipError_t raise_lds_limit(const void* kern, int bytes, std::atomic<uint6
   return e;
 }
 
+// CUs of the current device, asked for once per device (0: an error)
+inline int cus_of_current() {
+  static std::atomic<int> known[64];
+  int dev = -1, n = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0) return 0;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 // canonical AoS blocks of an [N, K] matrix -> the tiled device layout of
 // layout.h (the destination holds layout_bytes(...) bytes)
 size_t layout_bytes(int qtype, int N, int K);

@@ -173,6 +173,29 @@ struct LogitsArgs {
 };
 hipError_t launch_logits(const LogitsArgs& a, int in_dtype, int out_dtype, int num_cu, hipStream_t st);
 
+constexpr int SAMPLE_BINS = 256;                  // of a slice's histogram
+struct SampleArgs {
+  const void* x;              // [rows][x_stride]
+  int64_t rows, vocab, x_stride;
+  const float* u;             // [rows]
+  const float* temperature;   // [rows] or null: 1
+  const int32_t* top_k;       // [rows] or null: all
+  const float* top_p;         // [rows] or null: 1
+  const float* min_p;         // [rows] or null: 0
+  int32_t* out;               // [rows]
+  float* logprobs;            // [rows] or null
+  unsigned long long* hist;   // [rows][slices][SAMPLE_BINS]
+  float* tops;                // [rows][slices]: the largest logits
+  int slices;
+};
+// tokens of a slice: few where larger ones would leave CUs idle
+inline int sample_slice(int64_t rows, int64_t vocab, int num_cu) {
+  int slice = 16384;
+  while (slice > 4096 && rows * ((vocab + slice - 1) / slice) < 2 * (int64_t)num_cu) slice /= 2;
+  return slice;
+}
+hipError_t launch_sample(const SampleArgs& a, int slice, int dtype, hipStream_t st);
+
 // ---- device helpers ----
 
 template <class E> struct Mat;

@@ -45,17 +45,6 @@ bool fail_workspace() {
   return p && (!strcmp(p, "all") || !strcmp(p, "workspace"));
 }
 
-// CUs of the current device, asked for once per device (0: an error)
-int cus_of_current() {
-  static std::atomic<int> known[64];
-  int dev = -1, n = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0) return 0;
-  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
-  if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
-  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
-
 int check_kv_device(const fc_gguf_kv* h) {
   int dev = -1;
   if (hipGetDevice(&dev) != hipSuccess) return FC_GGUF_EHIP;
@@ -339,7 +328,7 @@ int fc_gguf_logits(const void* x, int64_t x_stride, int dtype, int64_t rows, int
   if (mask && (!on(mask, 4) || mask_stride < (vocab + 31) / 32)) return FC_GGUF_EINVAL;
   if ((repetition && !on(repetition, 4)) || (frequency && !on(frequency, 4)) || (presence && !on(presence, 4)))
     return FC_GGUF_EINVAL;
-  const int num_cu = cus_of_current();
+  const int num_cu = fcg::cus_of_current();
   if (num_cu <= 0) return FC_GGUF_EHIP;
   fcg::LogitsArgs a = {};
   a.x = x;

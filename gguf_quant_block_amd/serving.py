@@ -395,3 +395,69 @@ def process_logits(x, *, tokens=None, lens=None, prompt_lens=None, repetition=No
     if rc != 0:
         _check(rc, "fc_gguf_logits")
     return out
+
+
+_workspaces = {}                                           # bytes that (device, rows, vocab) takes
+
+
+def sample(x, u, *, temperature=None, top_k=None, top_p=None, min_p=None, out=None, logprobs=None):
+    """The next token of each row of logits x [rows, vocab] (f16, bf16 or f32; rows may be strided) from random numbers
+    u f32 [rows] in [0, 1).  Of the tokens in decreasing order (ties by lowest id) the first top_k i32 [rows] are kept (0:
+    all), of these the shortest beginning that holds top_p f32 [rows] of their weight, of these the ones whose weight is
+    at least min_p f32 [rows] of the largest's; weights are exp(x / temperature), temperature f32 [rows] (1; 0: the
+    largest token).  Masked tokens (-inf) and NaN take no part; a row where nothing does gives -1.  Returns the ids in out i32 [rows]
+    (None: a new tensor); logprobs f32 [rows], to fill: the log of the chosen token's share of the kept weight, or None."""
+    dev, dtype = x.get_device(), DTYPES.get(x.dtype)
+    if dev < 0 or dtype is None or x.dim() != 2:
+        raise ValueError("x: f16, bf16 or f32 [rows, vocab] on the GPU")
+    rows, vocab = x.shape
+    xs, one = x.stride()
+    if one != 1 and vocab > 1:
+        raise ValueError("x: contiguous rows")
+    if rows <= 1:
+        xs = max(xs, vocab)
+    _floats(u, rows, dev, "u")
+    tp = kp = pp = mp = lp = None
+    if temperature is not None:
+        _floats(temperature, rows, dev, "temperature")
+        tp = temperature.data_ptr()
+    if top_k is not None:
+        _ints(top_k, dev, "top_k", 1)
+        _need(top_k.shape[0] == rows, "top_k: one for each row")
+        kp = top_k.data_ptr()
+    if top_p is not None:
+        _floats(top_p, rows, dev, "top_p")
+        pp = top_p.data_ptr()
+    if min_p is not None:
+        _floats(min_p, rows, dev, "min_p")
+        mp = min_p.data_ptr()
+    if logprobs is not None:
+        _floats(logprobs, rows, dev, "logprobs")
+        lp = logprobs.data_ptr()
+    if torch.cuda.current_device() != dev:
+        raise ValueError(f"x: on the current device, not on cuda:{dev}")
+    if out is None:
+        out = torch.empty(rows, dtype=torch.int32, device=x.device)
+    else:
+        _ints(out, dev, "out", 1)
+        _need(out.shape[0] == rows, "out: one for each row")
+    xp, up, op, n = x.data_ptr(), u.data_ptr(), out.data_ptr(), 4 * rows
+    end = xp + ((rows - 1) * xs + vocab) * (4 if dtype == F32 else 2)
+    for y in (op, lp):
+        if y is not None and (y < end and xp < y + n or any(z is not None and y < z + n and z < y + n for z in (up, tp, kp, pp, mp))):
+            raise ValueError("out and logprobs: no memory of the inputs")
+    if lp is not None and lp < op + n and op < lp + n:
+        raise ValueError("out and logprobs: not the same memory")
+    size = _workspaces.get((dev, rows, vocab))
+    if size is None:
+        size = _call("fc_gguf_sample_workspace")(rows, vocab)
+        _check(min(size, 0), "fc_gguf_sample_workspace")
+        if len(_workspaces) > 1000:
+            _workspaces.clear()
+        _workspaces[dev, rows, vocab] = size
+    # of this call alone: calls on other streams and in graphs have theirs
+    ws = torch.empty(size, dtype=torch.uint8, device=x.device)
+    rc = _call("fc_gguf_sample")(xp, xs, dtype, rows, vocab, up, tp, kp, pp, mp, op, lp, ws.data_ptr(), size, _stream(dev))
+    if rc != 0:
+        _check(rc, "fc_gguf_sample")
+    return out

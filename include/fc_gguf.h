@@ -457,6 +457,41 @@ int fc_gguf_logits(const void* x, int64_t x_stride, int dtype, int64_t rows, int
                    const float* bias_values, int64_t bias_count, const uint32_t* mask, int64_t mask_stride,
                    void* out, int64_t out_stride, int out_dtype, void* stream);
 
+/*
+ * The next token of each row of logits, from a given random number.
+ *   w_v      exp((x_v - largest x) / temperature)
+ *   order    decreasing x, ties by lowest id
+ *   kept     of that order the first top_k; of these the shortest beginning that
+ *            holds at least top_p of their weight; of these the tokens with
+ *            w_v >= min_p; but always the first
+ *   chosen   the first of the kept, in that order, whose running sum of weights
+ *            is greater than u times their sum (u >= 1: the last)
+ *   x            device [rows][vocab] of dtype (F16, BF16 or F32), row stride in
+ *                elements; -inf and NaN take no part, +inf leaves only its like
+ *   u            device f32[rows], in [0, 1) (below 0 or NaN: 0)
+ *   temperature  device f32[rows] or NULL (1); 0, negative or NaN: the first of
+ *                the order
+ *   top_k        device i32[rows] or NULL; 0 or negative: all
+ *   top_p        device f32[rows] or NULL; 1 or more or NaN: all
+ *   min_p        device f32[rows] or NULL; 0, negative or NaN: all
+ *   out          device i32[rows]: the chosen ids; -1 where no token takes part
+ *   logprobs     device f32[rows] or NULL: log of the chosen token's share of the
+ *                kept weight (-inf beside -1)
+ *   workspace    device memory, 8-byte aligned, of fc_gguf_sample_workspace's
+ *                bytes at least, for this call alone until it is done
+ * Weights are summed in whole numbers of 2^-33 of an octave, so that a row's
+ * result depends on that row alone and equal calls give equal bits.  rows <=
+ * 65535, vocab <= 2^24 (else ERANGE); rows == 0 is a no-op.  Runs on the current
+ * device.  out and logprobs must not overlap the inputs or the workspace.
+ */
+int fc_gguf_sample(const void* x, int64_t x_stride, int dtype, int64_t rows, int64_t vocab, const float* u,
+                   const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                   int32_t* out, float* logprobs, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of the workspace of such a call on the current device, or a negative
+ * FC_GGUF_E* code. */
+int64_t fc_gguf_sample_workspace(int64_t rows, int64_t vocab);
+
 /* Static description of an error code. */
 const char* fc_gguf_strerror(int code);
 
