@@ -13,8 +13,10 @@ constexpr int64_t kMaxRows = 65535, kMaxVocab = (int64_t)1 << 24;
 
 bool on(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
-// bytes of `rows` rows in slices: their histograms, then their largest logits
-size_t workspace_of(int64_t rows, int64_t slices) { return (size_t)(rows * slices) * (fcg::SAMPLE_BINS * 8 + 4); }
+// bytes of `rows` rows in slices: their histograms, their first tokens, their largest logits
+size_t workspace_of(int64_t rows, int64_t slices) {
+  return (size_t)(rows * slices) * ((fcg::SAMPLE_BINS + fcg::SAMPLE_FIRST) * 8 + sizeof(fcg::SliceTop));
+}
 
 }  // namespace
 
@@ -44,6 +46,7 @@ int fc_gguf_sample(const void* x, int64_t x_stride, int dtype, int64_t rows, int
   if (cus <= 0) return FC_GGUF_EHIP;
   const int slice = fcg::sample_slice(rows, vocab, cus);
   fcg::SampleArgs a = {};
+  a.slice = slice;
   a.slices = (int)((vocab + slice - 1) / slice);
   if (workspace_bytes < 0 || (size_t)workspace_bytes < workspace_of(rows, a.slices)) return FC_GGUF_EINVAL;
   a.x = x;
@@ -58,8 +61,9 @@ int fc_gguf_sample(const void* x, int64_t x_stride, int dtype, int64_t rows, int
   a.out = out;
   a.logprobs = logprobs;
   a.hist = (unsigned long long*)workspace;
-  a.tops = (float*)(a.hist + rows * a.slices * fcg::SAMPLE_BINS);
-  return fcg::launch_sample(a, slice, dtype, (hipStream_t)stream) == hipSuccess ? FC_GGUF_OK : FC_GGUF_EHIP;
+  a.first = (uint2*)(a.hist + rows * a.slices * fcg::SAMPLE_BINS);
+  a.slice_tops = (fcg::SliceTop*)(a.first + rows * a.slices * fcg::SAMPLE_FIRST);
+  return fcg::launch_sample(a, dtype, (hipStream_t)stream) == hipSuccess ? FC_GGUF_OK : FC_GGUF_EHIP;
 }
 
 }  // extern "C"

@@ -14,10 +14,8 @@ hipError_t hipDeviceGetAttribute(int* v, hipDeviceAttribute_t, int) { *v = cus; 
 }
 namespace fcg {
 static SampleArgs last;
-static int last_slice = 0;
-hipError_t launch_sample(const SampleArgs& a, int slice, int, hipStream_t) {
+hipError_t launch_sample(const SampleArgs& a, int, hipStream_t) {
   last = a;
-  last_slice = slice;
   ++launches;
   return hipSuccess;
 }
@@ -76,9 +74,10 @@ int main() {
         EXPECT(fc_gguf_sample(p, vocab, 0, rows, vocab, f, f, i, f, f, o, l, p, need, nullptr), 0, 1);
         const fcg::SampleArgs& a = fcg::last;
         const int64_t slices = a.slices;
-        if ((char*)(a.tops + rows * slices) > (char*)p + need || (char*)a.hist != (char*)p ||
-            (char*)(a.hist + rows * slices * fcg::SAMPLE_BINS) > (char*)a.tops || slices * fcg::last_slice < vocab ||
-            (slices - 1) * fcg::last_slice >= vocab || slices * 512 * rows >= (int64_t)1 << 42 || slices >= (int64_t)1 << 31) {
+        if ((char*)(a.slice_tops + rows * slices) > (char*)p + need || (char*)a.hist != (char*)p ||
+            (char*)(a.hist + rows * slices * fcg::SAMPLE_BINS) > (char*)a.first ||
+            (char*)(a.first + rows * slices * fcg::SAMPLE_FIRST) > (char*)a.slice_tops || slices * a.slice < vocab ||
+            (slices - 1) * a.slice >= vocab || slices * 512 * rows >= (int64_t)1 << 42 || slices >= (int64_t)1 << 31) {
           printf("rows %lld, vocab %lld: workspace\n", (long long)rows, (long long)vocab);
           return 1;
         }
