@@ -19,7 +19,9 @@
 //
 // Two launches: slices of rows over the whole card, then a workgroup for each
 // row.  A slice also writes down its first tokens, so that a row whose kept
-// tokens are few, as they mostly are, is not read again.
+// tokens are few, as they mostly are, is not read again.  Where it has to be,
+// for the bins in which something ends, the workgroups that the rows leave idle
+// read parts of it, and the one that is done last goes on with what they found.
 #include <math.h>
 
 #include "serving.h"
@@ -34,8 +36,10 @@ constexpr int COUNT_SHIFT = 49;                // a slice's bin: the sum of M be
 constexpr int SLICE_MOST = 16384;              // (2^14 tokens of less than 2^34 would be 2^48)
 constexpr int FIRST = SAMPLE_FIRST;            // tokens that a slice writes down, at most
 constexpr int FIRST_WANTED = FIRST - 16;
-constexpr int LIST = 8192;                     // tokens that are looked at from LDS
-constexpr int FEW = 512;                       // that are ranked against each other
+constexpr int LIST = 4096;                     // tokens that are looked at from LDS
+constexpr int PART = SAMPLE_PART;              // of those that a workgroup of a row hands over
+constexpr int FEW = 512;                       // tokens of a row that are ranked against each other at once,
+constexpr int FEW_OF_BIN = 128;                // and of a bin, with their sums (each against all: 10 us for 512)
 
 // N values at an address aligned to one of them
 template <class T, int N> struct Some { typedef T vec __attribute__((ext_vector_type(N), aligned(sizeof(T)))); };
@@ -256,6 +260,7 @@ __global__ __launch_bounds__(512) void sample_slice_kernel(SampleArgs a) {
   }
   __syncthreads();
   if (tid == 0) {
+    if (blockIdx.x == 0) a.arrived[row] = 0;
     const uint32_t n = first_n;
     a.slice_tops[slice] = n <= (uint32_t)FIRST ? SliceTop{top, (uint16_t)bins, (uint16_t)n} : SliceTop{top, 0, 0};
   }
@@ -284,10 +289,12 @@ struct RowChoice {
     int its_bin[KNOWN];                        // of the slices: the bin of their largest logit,
     int its_end[KNOWN];                        // the first bin whose tokens they did not write down,
     int its_n[KNOWN];                          // and how many they wrote
-    u64 few[FEW], few_m[FEW], few_before[FEW];
+    u64 few[FEW], few_m[FEW_OF_BIN], few_before[FEW_OF_BIN];
     uint32_t few_rank[FEW];
     float wave_top[THREADS / 64];
     uint32_t n;                                // tokens of a list
+    uint32_t arrived;
+    uint32_t part_n[SAMPLE_MOST_PARTS];
     int found;
     Beginning got;
     u64 total_sum;
@@ -304,7 +311,7 @@ struct RowChoice {
   float top;
   double top_q;          // of the largest logit
   int list_n;            // tokens of the list
-  int list_from, list_to;   // the bins that it holds
+  int list_from[2], list_to[2];   // the bins that it holds: two stretches
   uint2 ahead[AHEAD];
 
   // bin of a token, BINS: of none
@@ -413,15 +420,85 @@ struct RowChoice {
     }
     __syncthreads();
     list_n = (int)(s.n < (uint32_t)LIST ? s.n : (uint32_t)LIST);
-    list_from = from;
-    list_to = to;
+    hold(from, to, 0, -1);
+  }
+  __device__ __forceinline__ void hold(int from, int to, int from2, int to2) {
+    list_from[0] = from;
+    list_to[0] = to;
+    list_from[1] = from2;
+    list_to[1] = to2;
+  }
+  __device__ __forceinline__ bool holds(int bin) const {
+    return (list_from[0] <= bin && bin <= list_to[0]) || (list_from[1] <= bin && bin <= list_to[1]);
+  }
+
+  // whether the slices wrote down all tokens of bins up to `to`
+  __device__ __forceinline__ bool written(int to) const {
+    bool read = false;
+    for (int i = tid & 63; i < a.slices; i += 64) {
+      int bin, end, many;
+      slice_bins(i, bin, end, many);
+      read = read || (bin <= to && end <= to);
+    }
+    return !__any(read);
+  }
+
+  // The list of two stretches of bins, [from, to] before [from2, to2] (the latter
+  // may be empty), each workgroup of the row reading a part of it: true in the one
+  // that has the whole list, the last to be done.
+  __device__ __forceinline__ bool gather_parts(int from, int to, int from2, int to2) {
+    const int parts = gridDim.x, part = blockIdx.x;
+    __syncthreads();
+    if (tid == 0) s.n = 0;
+    __syncthreads();
+    const float low = lowest_of(to, top, top_q, set.c4).out, high = from == 0 ? INFINITY : lowest_of(from - 1, top, top_q, set.c4).in;
+    const float low2 = to2 < from2 ? INFINITY : lowest_of(to2, top, top_q, set.c4).out;
+    const float high2 = to2 < from2 ? -INFINITY : lowest_of(from2 - 1, top, top_q, set.c4).in;
+    const int64_t each = ((a.vocab + parts - 1) / parts + 7) / 8 * 8, v0 = part * each, v1 = v0 + each;
+    if (v0 < a.vocab)
+      each_above(v0, v1 < a.vocab ? v1 : a.vocab, low < low2 ? low : low2, [&](float v, uint32_t id) {
+        if (!((v >= low && v <= high) || (v >= low2 && v <= high2))) return;
+        const int d = bin_below(q_below(v, top, set.c4), top_q);
+        if (!((d >= from && d <= to) || (d >= from2 && d <= to2))) return;
+        const uint32_t i = atomicAdd(&s.n, 1u);
+        if (i < (uint32_t)LIST) s.list[i] = order_of(v, id);
+      });
+    __syncthreads();
+    list_n = (int)s.n;
+    if (parts > 1) {
+      // handed over by stores and loads past the XCDs' caches; a part that found more than there is room for says so
+      u64* mine = a.parts + (row * parts + part) * PART;
+      for (int i = tid; i < list_n && i < PART; i += THREADS) __hip_atomic_store(mine + i, s.list[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (tid == 0) __hip_atomic_store(a.part_n + row * parts + part, (uint32_t)list_n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      if (tid == 0) s.arrived = __hip_atomic_fetch_add(a.arrived + row, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __syncthreads();
+      if (s.arrived != (uint32_t)parts - 1) return false;
+      if (tid < parts) s.part_n[tid] = __hip_atomic_load(a.part_n + row * parts + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __syncthreads();
+      for (int k = 0; k < parts; ++k) {
+        const int n = (int)s.part_n[k];
+        if (n > PART || (k != part && list_n + n > LIST)) {       // (bins will be gathered one by one)
+          hold(0, -1, 0, -1);
+          return true;
+        }
+        if (k == part) continue;
+        const u64* its = a.parts + (row * parts + k) * PART;
+        for (int i = tid; i < n; i += THREADS) s.list[list_n + i] = __hip_atomic_load(its + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        list_n += n;
+      }
+      __syncthreads();
+    }
+    hold(from, to, from2, to2);
+    return true;
   }
 
   // f(x, id, M) of every token of a bin: from the list, into which its tokens go
   // if they fit it, or from the row
   template <class F>
   __device__ __forceinline__ void each_of(int bin, F f) {
-    if (list_from <= bin && bin <= list_to) {
+    if (holds(bin)) {
       for (int i = tid; i < list_n; i += THREADS) {
         const u64 o = s.list[i];
         u64 m;
@@ -430,14 +507,14 @@ struct RowChoice {
       }
       return;
     }
-    const float low = lowest_of(bin, top, top_q, set.c4).out;
+    const float low = lowest_of(bin, top, top_q, set.c4).out, high = bin == 0 ? INFINITY : lowest_of(bin - 1, top, top_q, set.c4).in;
     each_above(0, a.vocab, low, [&](float v, uint32_t id) {
       u64 m;
-      if (bin_of(v, m) == bin) f(v, id, m);
+      if (v <= high && bin_of(v, m) == bin) f(v, id, m);
     });
   }
   __device__ __forceinline__ void see_to(int bin) {
-    if (!(list_from <= bin && bin <= list_to) && s.count[bin] <= LIST) gather(bin, bin);
+    if (!holds(bin) && s.count[bin] <= LIST) gather(bin, bin);
   }
 
   // Ranks `few` tokens of s.few against each other: how many are before each, and, of SUMS, their M.
@@ -471,12 +548,12 @@ struct RowChoice {
     see_to(bin);
     uint32_t had = 0, n = s.count[bin];        // tokens before those that are left, and how many these are
     u64 had_sum = 0, lo = 0, hi = ~0ull;       // sum before them, and their range
-    if (n > FEW && top < INFINITY) {           // (at first all that is outside a narrower range goes to its ends)
+    if (n > FEW_OF_BIN && top < INFINITY) {           // (at first all that is outside a narrower range goes to its ends)
       hi = order_of(lowest_of(bin, top, top_q, set.c4).out, ~0u);
       lo = order_of(lowest_of(bin - 1, top, top_q, set.c4).in, 0);
     }
     bool first = true;
-    while (n > FEW) {
+    while (n > FEW_OF_BIN) {
       // 256 ways
       const u64 range = hi - lo;
       const int bits = 64 - __builtin_clzll(range | 1), shift = bits > 8 ? bits - 8 : 0;
@@ -547,7 +624,7 @@ struct RowChoice {
     // those that are left, each against all
     __syncthreads();
     if (tid == 0) s.n = 0;
-    if (tid < FEW) {
+    if (tid < FEW_OF_BIN) {
       s.few_before[tid] = 0;
       s.few_rank[tid] = 0;
     }
@@ -556,13 +633,13 @@ struct RowChoice {
       const u64 o = order_of(v, id);
       if (o < lo || o > hi) return;
       const uint32_t i = atomicAdd(&s.n, 1u);
-      if (i < (uint32_t)FEW) {
+      if (i < (uint32_t)FEW_OF_BIN) {
         s.few[i] = o;
         s.few_m[i] = m;
       }
     });
     __syncthreads();
-    const int few = (int)(s.n < (uint32_t)FEW ? s.n : (uint32_t)FEW);
+    const int few = (int)(s.n < (uint32_t)FEW_OF_BIN ? s.n : (uint32_t)FEW_OF_BIN);
     rank<true>(few);
     __syncthreads();
     if (tid < few) {
@@ -793,36 +870,88 @@ struct RowChoice {
       if (by_weight) last = reach(set.top_p * all, false);
       if (least_bin < last) last = least_bin;
     }
-    const int count_bin = last;
     list_n = 0;
-    list_from = 0;
-    list_to = -1;
-    const uint32_t upto = s.count_before[last + 1];
-    if (upto <= (uint32_t)LIST) gather(0, last);
-    if (upto <= (uint32_t)FEW) {
+    hold(0, -1, 0, -1);
+    if (s.count_before[last + 1] <= (uint32_t)FEW) {
+      if (blockIdx.x) return;
+      gather(0, last);
       choose_of_few(by_count, by_weight, least, all);
+      return;
+    }
+
+    // The bins in which something ends, [b0, b1], and with them the range of the
+    // kept weight, [least_sum, most_sum], and so of the bin of the token, [t0, t1].
+    const int count_bin = last;
+    bool for_count = by_count, for_weight = by_weight;
+    int b0 = BINS, b1 = -1, end_bin = BINS - 1;
+    double least_sum = all, most_sum = all;
+    if (by_count) {
+      b0 = b1 = end_bin = count_bin;
+      least_sum = s.before[count_bin];
+      most_sum = s.before[count_bin + 1];
+    }
+    if (by_weight) {
+      const double g0 = set.top_p * least_sum, g1 = set.top_p * most_sum;
+      int d0 = reach(g0 > 1e-300 ? g0 : 1e-300, false), d1 = reach(g1, false);
+      d0 = d0 < end_bin ? d0 : end_bin;
+      d1 = d1 < end_bin ? d1 : end_bin;
+      b0 = d0 < b0 ? d0 : b0;
+      b1 = d1 > b1 ? d1 : b1;
+      end_bin = d1;
+      least_sum = g0;
+      most_sum = most_sum < s.before[d1 + 1] ? most_sum : s.before[d1 + 1];
+    }
+    const bool for_least = least_bin <= end_bin;
+    if (for_least) {
+      if (least_bin < b0) {                    // it leaves less than the others, wherever these end
+        for_count = for_weight = false;
+        b0 = b1 = least_bin;
+      }
+      b1 = least_bin > b1 ? least_bin : b1;
+      end_bin = least_bin;
+      least_sum = least_sum < s.before[least_bin] ? least_sum : s.before[least_bin];
+      most_sum = most_sum < s.before[least_bin + 1] ? most_sum : s.before[least_bin + 1];
+    }
+    const double short_of_all = all * (1.0 - 0x1p-52), u1 = set.u * most_sum;
+    int t0 = reach(set.u * least_sum < short_of_all ? set.u * least_sum : short_of_all, true);
+    int t1 = reach(u1 < short_of_all ? u1 : short_of_all, true);
+    t1 = t1 < end_bin ? t1 : end_bin;
+    t0 = t0 < t1 ? t0 : t1;
+    if (b1 >= 0 && t1 >= b0 - 1) {             // one stretch
+      t0 = t0 < b0 ? t0 : b0;
+      t1 = b1 > t1 ? b1 : t1;
+      b0 = 0;
+      b1 = -1;
+    } else if (b1 < 0) {
+      b0 = 0;
+    }
+    const uint32_t many = s.count_before[t1 + 1] - s.count_before[t0] + (b1 >= b0 ? s.count_before[b1 + 1] - s.count_before[b0] : 0);
+    if (s.count_before[last + 1] <= (uint32_t)LIST && written(last)) {
+      if (blockIdx.x) return;
+      gather(0, last);
+    } else if (many <= (uint32_t)LIST) {
+      if (!gather_parts(t0, t1, b0, b1)) return;
+    } else if (blockIdx.x) {
       return;
     }
 
     // (a beginning that ends in no bin of its own: all of them)
     Beginning kept = {BINS - 1, s.count[BINS - 1], s.sum[BINS - 1], 0};
-    if (by_count) {
+    if (for_count) {
       const uint32_t c = (uint32_t)set.top_k - s.count_before[count_bin];
       kept = c < s.count[count_bin] ? select(count_bin, c, 0) : Beginning{count_bin, c, s.sum[count_bin], 0};
     }
-    if (by_weight) {
+    if (for_weight) {
       const double g = set.top_p * (by_count ? weight(kept) : all);
       int d = reach(g < all ? g : all, false);
       if (d > kept.bin) d = kept.bin;
-      if (d <= last) {                         // (past it min_p leaves less)
-        const u64 most = d == kept.bin ? kept.sum : s.sum[d];
-        double need = ceil((g - s.before[d]) / unit_of(d));
-        need = need < 1.0 ? 1.0 : need;
-        if (need < (double)most) kept = select(d, 0, (u64)need);
-        else if (d < kept.bin) kept = {d, s.count[d], s.sum[d], 0};
-      }
+      const u64 most = d == kept.bin ? kept.sum : s.sum[d];
+      double need = ceil((g - s.before[d]) / unit_of(d));
+      need = need < 1.0 ? 1.0 : need;
+      if (need < (double)most) kept = select(d, 0, (u64)need);
+      else if (d < kept.bin) kept = {d, s.count[d], s.sum[d], 0};
     }
-    if (least_bin < BINS && least_bin <= kept.bin) {
+    if (for_least && least_bin <= kept.bin) {
       see_to(least_bin);
       __syncthreads();
       if (tid == 0) {
@@ -863,7 +992,7 @@ struct RowChoice {
 template <class I>
 __global__ __launch_bounds__(1024) void sample_choose_kernel(SampleArgs a) {
   __shared__ typename RowChoice<I>::Shared shared;
-  const int64_t row = blockIdx.x;
+  const int64_t row = blockIdx.y;
   RowChoice<I> r{a, shared, (int)threadIdx.x, row, (const I*)a.x + row * a.x_stride};
   r.run();
 }
@@ -875,7 +1004,7 @@ hipError_t launch_i(const SampleArgs& a, hipStream_t st) {
   if (a.slice == 4096) e = launch_kernel(sample_slice_kernel<I, 2>, grid, 512, 0, st, a);
   else e = launch_kernel(sample_slice_kernel<I, 4>, grid, 512, 0, st, a);
   if (e != hipSuccess) return e;
-  return launch_kernel(sample_choose_kernel<I>, dim3((unsigned)a.rows), 1024, 0, st, a);
+  return launch_kernel(sample_choose_kernel<I>, dim3((unsigned)a.row_parts, (unsigned)a.rows), 1024, 0, st, a);
 }
 
 }  // namespace

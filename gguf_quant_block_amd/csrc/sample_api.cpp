@@ -13,10 +13,25 @@ constexpr int64_t kMaxRows = 65535, kMaxVocab = (int64_t)1 << 24;
 
 bool on(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
-// bytes of `rows` rows in slices: their histograms, their first tokens, their largest logits
-size_t workspace_of(int64_t rows, int64_t slices) {
-  return (size_t)(rows * slices) * ((fcg::SAMPLE_BINS + fcg::SAMPLE_FIRST) * 8 + sizeof(fcg::SliceTop));
-}
+// How a call's workspace is divided: the slices' histograms, first tokens and
+// largest logits, then the lists that the parts of a row hand over, and counters.
+// (All of 8 bytes but the counters, which come last.)
+struct Division {
+  int slice, slices, parts;
+  size_t first, tops, lists, part_n, arrived, bytes;
+  Division(int64_t rows, int64_t vocab, int cus) {
+    slice = fcg::sample_slice(rows, vocab, cus);
+    slices = (int)((vocab + slice - 1) / slice);
+    parts = fcg::sample_parts(rows, vocab, cus);
+    const size_t n = (size_t)rows * slices, lists_n = parts > 1 ? (size_t)rows * parts : 0;
+    first = n * fcg::SAMPLE_BINS * 8;
+    tops = first + n * fcg::SAMPLE_FIRST * sizeof(uint2);
+    lists = tops + n * sizeof(fcg::SliceTop);
+    part_n = lists + lists_n * fcg::SAMPLE_PART * 8;
+    arrived = part_n + lists_n * 4;
+    bytes = arrived + (size_t)rows * 4;
+  }
+};
 
 }  // namespace
 
@@ -27,8 +42,7 @@ int64_t fc_gguf_sample_workspace(int64_t rows, int64_t vocab) {
   if (rows > kMaxRows || vocab > kMaxVocab) return FC_GGUF_ERANGE;
   const int cus = fcg::cus_of_current();
   if (cus <= 0) return FC_GGUF_EHIP;
-  const int slice = fcg::sample_slice(rows, vocab, cus);
-  return (int64_t)workspace_of(rows, (vocab + slice - 1) / slice);
+  return (int64_t)Division(rows, vocab, cus).bytes;
 }
 
 int fc_gguf_sample(const void* x, int64_t x_stride, int dtype, int64_t rows, int64_t vocab, const float* u,
@@ -44,11 +58,12 @@ int fc_gguf_sample(const void* x, int64_t x_stride, int dtype, int64_t rows, int
     return FC_GGUF_EINVAL;
   const int cus = fcg::cus_of_current();
   if (cus <= 0) return FC_GGUF_EHIP;
-  const int slice = fcg::sample_slice(rows, vocab, cus);
+  const Division d(rows, vocab, cus);
+  if (workspace_bytes < 0 || (size_t)workspace_bytes < d.bytes) return FC_GGUF_EINVAL;
   fcg::SampleArgs a = {};
-  a.slice = slice;
-  a.slices = (int)((vocab + slice - 1) / slice);
-  if (workspace_bytes < 0 || (size_t)workspace_bytes < workspace_of(rows, a.slices)) return FC_GGUF_EINVAL;
+  a.slice = d.slice;
+  a.slices = d.slices;
+  a.row_parts = d.parts;
   a.x = x;
   a.x_stride = x_stride;
   a.rows = rows;
@@ -60,9 +75,13 @@ int fc_gguf_sample(const void* x, int64_t x_stride, int dtype, int64_t rows, int
   a.min_p = min_p;
   a.out = out;
   a.logprobs = logprobs;
-  a.hist = (unsigned long long*)workspace;
-  a.first = (uint2*)(a.hist + rows * a.slices * fcg::SAMPLE_BINS);
-  a.slice_tops = (fcg::SliceTop*)(a.first + rows * a.slices * fcg::SAMPLE_FIRST);
+  char* const w = (char*)workspace;
+  a.hist = (unsigned long long*)w;
+  a.first = (uint2*)(w + d.first);
+  a.slice_tops = (fcg::SliceTop*)(w + d.tops);
+  a.parts = (unsigned long long*)(w + d.lists);
+  a.part_n = (uint32_t*)(w + d.part_n);
+  a.arrived = (uint32_t*)(w + d.arrived);
   return fcg::launch_sample(a, dtype, (hipStream_t)stream) == hipSuccess ? FC_GGUF_OK : FC_GGUF_EHIP;
 }
 

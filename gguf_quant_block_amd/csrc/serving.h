@@ -174,7 +174,9 @@ struct LogitsArgs {
 hipError_t launch_logits(const LogitsArgs& a, int in_dtype, int out_dtype, int num_cu, hipStream_t st);
 
 constexpr int SAMPLE_BINS = 256;                  // of a slice's histogram
-constexpr int SAMPLE_FIRST = 64;                  // tokens that a slice writes down
+constexpr int SAMPLE_FIRST = 128;                 // tokens that a slice writes down
+constexpr int SAMPLE_PART = 2048;                 // tokens that a part of a row hands over
+constexpr int SAMPLE_MOST_PARTS = 16;
 struct SliceTop {
   float top;                  // its largest logit
   uint16_t bins;              // bins whose tokens are all among those written down
@@ -193,12 +195,24 @@ struct SampleArgs {
   unsigned long long* hist;   // [rows][slices][SAMPLE_BINS]
   uint2* first;               // [rows][slices][SAMPLE_FIRST]: logits and ids
   SliceTop* slice_tops;       // [rows][slices]
+  unsigned long long* parts;  // [rows][row_parts][SAMPLE_PART]: tokens that a part of a row holds
+  uint32_t* part_n;           // [rows][row_parts]: how many
+  uint32_t* arrived;          // [rows]: parts that are done
   int slice, slices;          // tokens of a slice, slices of a row
+  int row_parts;              // workgroups that choose a row's token
 };
 // Tokens of a slice: few where larger ones would leave CUs idle.  (128 rows of
 // 131073 f32, both launches: slices of 4096 59 us, of 8192 52, of 16384 54.)
 inline int sample_slice(int64_t rows, int64_t vocab, int num_cu) {
   return rows * ((vocab + 8191) / 8192) < 2 * (int64_t)num_cu ? 4096 : 8192;
+}
+// Workgroups that choose a row's token: those that would be idle, a slice's
+// tokens for each at least.
+inline int sample_parts(int64_t rows, int64_t vocab, int num_cu) {
+  int64_t n = num_cu / (rows > 0 ? rows : 1);
+  const int64_t most = (vocab + 8191) / 8192;
+  n = n < most ? n : most;
+  return (int)(n < 1 ? 1 : n < SAMPLE_MOST_PARTS ? n : SAMPLE_MOST_PARTS);
 }
 hipError_t launch_sample(const SampleArgs& a, int dtype, hipStream_t st);
 

@@ -74,7 +74,10 @@ int main() {
         EXPECT(fc_gguf_sample(p, vocab, 0, rows, vocab, f, f, i, f, f, o, l, p, need, nullptr), 0, 1);
         const fcg::SampleArgs& a = fcg::last;
         const int64_t slices = a.slices;
-        if ((char*)(a.slice_tops + rows * slices) > (char*)p + need || (char*)a.hist != (char*)p ||
+        const int64_t parts = a.row_parts > 1 ? a.row_parts : 0;
+        if ((char*)(a.arrived + rows) > (char*)p + need || (char*)a.hist != (char*)p ||
+            (char*)(a.slice_tops + rows * slices) > (char*)a.parts || a.row_parts < 1 || a.row_parts > fcg::SAMPLE_MOST_PARTS ||
+            (char*)(a.parts + rows * parts * fcg::SAMPLE_PART) > (char*)a.part_n || a.part_n + rows * parts > a.arrived ||
             (char*)(a.hist + rows * slices * fcg::SAMPLE_BINS) > (char*)a.first ||
             (char*)(a.first + rows * slices * fcg::SAMPLE_FIRST) > (char*)a.slice_tops || slices * a.slice < vocab ||
             (slices - 1) * a.slice >= vocab || slices * 512 * rows >= (int64_t)1 << 42 || slices >= (int64_t)1 << 31) {
