@@ -143,9 +143,15 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
   // pieces of keys and of values on their way to LDS
   Raw kraw[NI], vraw[NI];
   u32x4 vst[NI];
-  // Q8: the stored exponents of the lane's key, and of the 8 keys of each piece of values
+  // Q8: the stored exponents of the lane's key, and of the 8 keys of each piece
+  // of values.  A wave's pieces are of 8 / WAVES times 8 keys, so that but for 96
+  // dimensions these are the same in every lane and taken apart once, by scalar
+  // instructions (by vector instructions for each piece: 4096 tokens over 8192
+  // keys 444 us instead of XXX).
+  constexpr bool SAME = D % 64 == 0;
+  constexpr int VG = SAME ? 8 / WAVES : NI;
   uint32_t ke = 0;
-  uint2 ve[NI];
+  uint2 ve[VG];
   // where the scales of a page that begins `start` bytes into the pool begin: a byte for D
   auto scales_at = [&](const uint8_t* scales, uint64_t start, int key) -> const uint8_t* {
     return scales + start / D + (uint32_t)(hk * ps + (key & (ps - 1)));
@@ -163,18 +169,26 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
     if constexpr (Q8) ke = *scales_at(a.kv.k_scale, start, tok0 + lane);
   };
   auto load_v = [&](int tok0, uint64_t start) {
+    if constexpr (Q8 && SAME)
+#pragma unroll
+      for (int i = 0; i < VG; ++i) {
+        const int k8 = wave * VG + i;
+        uint64_t at = start;
+        if constexpr (!BIG)
+          at = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(start >> 32), k8 * 8) << 32 | (uint32_t)__builtin_amdgcn_readlane((int)start, k8 * 8);
+        ve[i] = *(const uint2*)scales_at(a.kv.v_scale, at, tok0 + k8 * 8);
+      }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       if constexpr (BIG) {                       // pieces of a page follow each other
         vraw[i] = *(const Raw*)(vbase + start + (uint32_t)((tok0 & (ps - 1)) * (D * B) + (wave * NI + i) * 512 * B) + (uint32_t)lane * 8 * B);
-        if constexpr (Q8) ve[i] = *(const uint2*)scales_at(a.kv.v_scale, start, tok0 + ((wave * NI + i) * 64 + (D % 64 ? lane : 0)) / D * 8);
+        if constexpr (Q8 && !SAME) ve[i] = *(const uint2*)scales_at(a.kv.v_scale, start, tok0 + ((wave * NI + i) * 64 + lane) / D * 8);
       } else if constexpr (D % 64 == 0) {        // the wave's 64 pieces are of the same 8 keys
         const int p = (wave * NI + i) * 64, k8 = p / D, d = p - k8 * D;
         const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(start >> 32), k8 * 8) << 32 |
                             (uint32_t)__builtin_amdgcn_readlane((int)start, k8 * 8);
         const uint8_t* vp = vbase + at + (uint32_t)(((tok0 + k8 * 8) & (ps - 1)) * (D * B) + d * 8 * B);
         vraw[i] = *(const Raw*)(vp + (uint32_t)lane * 8 * B);
-        if constexpr (Q8) ve[i] = *(const uint2*)scales_at(a.kv.v_scale, at, tok0 + k8 * 8);
       } else {
         const int p = (wave * NI + i) * 64 + lane, k8 = p / D, d = p - k8 * D;
         const uint64_t at = __shfl(start, k8 * 8);
@@ -224,8 +238,17 @@ __global__ __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) void attend_tile_kern
   // A masked key's weight is 0, which must not meet an infinite or NaN value:
   // of tiles with masked keys those are stored as 0 and added at the end.
   auto clean = [&](int tok0, uint64_t ok) {
+    if constexpr (Q8 && SAME) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) vst[i] = piece_of(vraw[i], ve[i]);
+      for (int g = 0; g < VG; ++g) {
+        const ValueScales<E> scales(make_uint2(__builtin_amdgcn_readfirstlane(ve[g].x), __builtin_amdgcn_readfirstlane(ve[g].y)));
+#pragma unroll
+        for (int i = g * NI / VG; i < (g + 1) * NI / VG; ++i) vst[i] = scales.values(vraw[i].x, vraw[i].y);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) vst[i] = piece_of(vraw[i], ve[SAME ? 0 : i]);
+    }
     if (is_open(tok0, ok, t.lo, t.hi)) return;
     if (ok != ~0ull)
 #pragma unroll
