@@ -135,6 +135,12 @@ __device__ __forceinline__ Settings settings_of(const SampleArgs& a, int64_t row
   return s;
 }
 
+// whether something but u ends the row's kept tokens: only then are the first ones of use
+__device__ __forceinline__ bool ends_early(const SampleArgs& a, int64_t row) {
+  return (a.temperature && !(a.temperature[row] > 0.f)) || (a.top_k && a.top_k[row] > 0) || (a.top_p && a.top_p[row] < 1.f) ||
+         (a.min_p && a.min_p[row] > 0.f);
+}
+
 // The order of tokens: smaller is earlier.
 __device__ __forceinline__ u64 order_of(float x, uint32_t id) {
   const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.f);          // (-0 as 0)
@@ -143,6 +149,17 @@ __device__ __forceinline__ u64 order_of(float x, uint32_t id) {
 __device__ __forceinline__ float logit_of(u64 order) {
   const uint32_t b = (uint32_t)(order >> 32);
   return __builtin_bit_cast(float, b >> 31 ? b : ~b ^ 0x80000000u);
+}
+
+// The sum over this lane and those before it, by moves between lanes.
+__device__ __forceinline__ uint32_t running_sum(uint32_t x) {
+  x += __builtin_amdgcn_update_dpp(0, (int)x, 0x111, 0xF, 0xF, false);    // rows of 16 lanes: from 1, 2, 4 and 8 lanes before
+  x += __builtin_amdgcn_update_dpp(0, (int)x, 0x112, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, (int)x, 0x114, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, (int)x, 0x118, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, (int)x, 0x142, 0xA, 0xF, false);    // to rows 1 and 3 from the row before,
+  x += __builtin_amdgcn_update_dpp(0, (int)x, 0x143, 0xC, 0xF, false);    // to rows 2 and 3 from row 1
+  return x;
 }
 
 __device__ __forceinline__ float larger(float a, float b) { return a > b ? a : b; }
@@ -155,7 +172,6 @@ __global__ __launch_bounds__(512) void sample_slice_kernel(SampleArgs a) {
   static_assert(SLICE <= SLICE_MOST, "sums");
   __shared__ u64 hist[BINS];
   __shared__ float wave_top[THREADS / 64];
-  __shared__ int first_bins;
   __shared__ uint32_t first_n;
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.y, v0 = (int64_t)blockIdx.x * SLICE;
@@ -209,54 +225,51 @@ __global__ __launch_bounds__(512) void sample_slice_kernel(SampleArgs a) {
   __syncthreads();
   const int64_t slice = row * a.slices + blockIdx.x;
   if (tid < BINS) a.hist[slice * BINS + tid] = hist[tid];
-  if (tid < 64) {                              // bins whose tokens are FIRST_WANTED at most, from the top on
-    int c[4], c4 = 0, bins = 0;
+  // bins whose tokens are FIRST_WANTED at most, from the top on (every wave for itself)
+  const bool of_use = ends_early(a, row);
+  int bins = 0;
+  if (of_use) {
+    const int lane = tid & 63;
+    uint32_t c[4], all4 = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      c[k] = (int)(hist[4 * tid + k] >> COUNT_SHIFT);
-      c4 += c[k];
+      c[k] = (uint32_t)(hist[4 * lane + k] >> COUNT_SHIFT);
+      all4 += c[k];
     }
-    int cs = c4;
-#pragma unroll
-    for (int k = 1; k < 64; k *= 2) {
-      const int cu = __shfl_up(cs, k);
-      if (tid >= k) cs += cu;
-    }
-    cs -= c4;
+    uint32_t upto = running_sum(all4) - all4;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      cs += c[k];
-      bins += __builtin_popcountll(__ballot(cs <= FIRST_WANTED));
+      upto += c[k];
+      bins += __builtin_popcountll(__ballot(upto <= (uint32_t)FIRST_WANTED));
     }
-    if (tid == 0) first_bins = bins;
   }
-  __syncthreads();
   // What is below the bound of these bins is not in them; a few others that are
   // not may be written down too, while there is room.
-  const int bins = first_bins;
   float low = INFINITY;
   if (bins > 0 && top > -INFINITY) low = fmaxf(lowest_of(bins - 1, top, top_q, c4).out, -3.4028234663852886e38f);
-  if (low < INFINITY || top == INFINITY) {
-    // (a place for all of a wave's at once: one for each token cost 6 us of 29 for 128 rows of 131073)
+  if (bins > 0) {
+    // (a place for all of a wave's at once; one for each token cost 5 us of 29 for 128 rows of 131073)
     u64 those[4 * ROUNDS];
-    int many = 0;
+    uint32_t many = 0;
 #pragma unroll
     for (int k = 0; k < 4 * ROUNDS; ++k) {
       those[k] = __ballot(z[k] >= low);
       many += __builtin_popcountll(those[k]);
     }
     uint32_t at = 0;
-    if ((tid & 63) == 0) at = atomicAdd(&first_n, (uint32_t)many);
+    if ((tid & 63) == 0) at = atomicAdd(&first_n, many);
     at = __builtin_amdgcn_readfirstlane(at);
     uint2* first = a.first + slice * FIRST;
+    const uint32_t id = (uint32_t)v0 + tid * 4;
+    if (at + many <= (uint32_t)FIRST)
 #pragma unroll
-    for (int k = 0; k < 4 * ROUNDS; ++k)
-      if (those[k]) {
-        const uint32_t i = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(those[k] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)those[k], 0));
-        if (z[k] >= low && i < (uint32_t)FIRST)
-          first[i] = make_uint2(__builtin_bit_cast(uint32_t, z[k]), (uint32_t)v0 + (k / 4 * THREADS + tid) * 4 + k % 4);
-        at += __builtin_popcountll(those[k]);
-      }
+      for (int k = 0; k < 4 * ROUNDS; ++k)
+        if (those[k]) {
+          const uint32_t i = __builtin_amdgcn_mbcnt_hi((uint32_t)(those[k] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)those[k], at));
+          if (__builtin_amdgcn_inverse_ballot_w64(those[k]))
+            first[i] = make_uint2(__builtin_bit_cast(uint32_t, z[k]), id + k / 4 * THREADS * 4 + k % 4);
+          at += __builtin_popcountll(those[k]);
+        }
   }
   __syncthreads();
   if (tid == 0) {
@@ -872,9 +885,15 @@ struct RowChoice {
     }
     list_n = 0;
     hold(0, -1, 0, -1);
-    if (s.count_before[last + 1] <= (uint32_t)FEW) {
+    const uint32_t upto = s.count_before[last + 1];
+    const bool in_slices = upto <= (uint32_t)LIST && written(last);
+    if (in_slices) {
       if (blockIdx.x) return;
       gather(0, last);
+    }
+    if (upto <= (uint32_t)FEW) {
+      if (!in_slices && !gather_parts(0, last, 0, -1)) return;
+      if (!holds(last)) gather(0, last);
       choose_of_few(by_count, by_weight, least, all);
       return;
     }
@@ -926,13 +945,12 @@ struct RowChoice {
       b0 = 0;
     }
     const uint32_t many = s.count_before[t1 + 1] - s.count_before[t0] + (b1 >= b0 ? s.count_before[b1 + 1] - s.count_before[b0] : 0);
-    if (s.count_before[last + 1] <= (uint32_t)LIST && written(last)) {
-      if (blockIdx.x) return;
-      gather(0, last);
-    } else if (many <= (uint32_t)LIST) {
-      if (!gather_parts(t0, t1, b0, b1)) return;
-    } else if (blockIdx.x) {
-      return;
+    if (!in_slices) {
+      if (many <= (uint32_t)LIST) {
+        if (!gather_parts(t0, t1, b0, b1)) return;
+      } else if (blockIdx.x) {
+        return;
+      }
     }
 
     // (a beginning that ends in no bin of its own: all of them)
