@@ -48,9 +48,9 @@ namespace {
 // of the second dimension 32 (d / 2) + 2r + d % 2.  A lane still ends with the
 // scores of keys 8g .. 8g + 7, in another order.  Codes become values of E
 // where they are used, exactly (serving.h): what follows is the same.
-template <class E, int D, int RT, bool Q8>
+template <class E, int D, int RT, bool Q8, int WAVES>
 struct Piece {
-  static constexpr int KS = D / 32, DT = D / 16, AT_STEP = at_step(D);
+  static constexpr int KS = D / 32, DT = D / 16, AT_STEP = WAVES * AT_TILE;
   // where the score of the lane's key j stands: half, and element of it
   static constexpr int half_of(int j) { return Q8 ? j & 1 : j >> 2; }
   static constexpr int row_of(int j) { return Q8 ? j >> 1 : j & 3; }
@@ -272,11 +272,11 @@ struct Piece {
   }
 };
 
-// steps of at_step(D) keys of sequence s; 1 where its rows see no key or
+// steps of WAVES tiles of keys of sequence s; 1 where its rows see no key or
 // sequences are not split, 0 where it has no rows here
-template <int D>
+template <int WAVES>
 __device__ __forceinline__ int seq_steps(const AttendArgs& a, int s, int hk, RowTile& t) {
-  constexpr int AT_STEP = at_step(D);
+  constexpr int AT_STEP = WAVES * AT_TILE;
   if (s >= a.seqs || !row_tile(a, s, hk, 0, a.stream_rows, 1, a.stream_rows, AT_TILE, t)) return 0;
   return t.end > t.beg && !a.whole ? (t.end - t.beg + AT_STEP - 1) / AT_STEP : 1;
 }
@@ -302,10 +302,10 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 // Joins the pieces of a sequence's rows that workgroups x0 .. x1 left in the
 // workspace.  Four columns of a row are a thread's, in one pass with a running
 // maximum; while there are threads left the pieces are dealt to several.
-template <class E, int D>
+template <class E, int D, int WAVES>
 __device__ __forceinline__ void join_pieces(const AttendArgs& a, int q0, int rows, int hk, int x0, int x1, float* lds) {
   const __amdgpu_buffer_rsrc_t part = pieces_of(a.part), part_ml = pieces_of(a.part_ml);
-  constexpr int THREADS = at_waves(D) * 64, C4 = D / 4, AHEAD = 16;
+  constexpr int THREADS = WAVES * 64, C4 = D / 4, AHEAD = 16;
   const int tid = threadIdx.x, n = x1 - x0 + 1;
   // row `row` of piece i
   auto at = [&](int i, int row) -> uint32_t { return ((hk * a.shares + x0 + i) * 2 + (i == 0)) * a.stream_rows + row; };
@@ -380,9 +380,9 @@ __device__ __forceinline__ void join_pieces(const AttendArgs& a, int q0, int row
 // workgroup has two at most, the end of a sequence (or its middle; slot 0) and
 // the beginning of one (slot 1).  They go to the workspace, and the workgroup
 // that brings a sequence's last piece joins them.
-template <class E, int D, int RT, bool Q8>
-__global__ __launch_bounds__(at_waves(D) * 64, at_waves(D) / 4) void attend_stream_kernel(AttendArgs a) {
-  constexpr int DT = D / 16, AT_WAVES = at_waves(D), AT_STEP = at_step(D);
+template <class E, int D, int RT, bool Q8, int AT_WAVES>
+__global__ __launch_bounds__(AT_WAVES * 64, at_waves(D) / 4) void attend_stream_kernel(AttendArgs a) {
+  constexpr int DT = D / 16, AT_STEP = AT_WAVES * AT_TILE;
   constexpr int PITCH = D + 4;                    // floats of a row in LDS
   __shared__ __attribute__((aligned(16))) float sums[AT_WAVES * 16 * PITCH];
   __shared__ float ml[AT_WAVES][RT * 16][2];
@@ -396,7 +396,7 @@ __global__ __launch_bounds__(at_waves(D) * 64, at_waves(D) / 4) void attend_stre
   int64_t total = a.whole ? a.seqs : 0;
   int mine = 0;                                   // steps of sequence `lane`
   for (int s0 = a.whole ? a.seqs : 0; s0 < a.seqs; s0 += 64) {
-    int n = seq_steps<D>(a, s0 + lane, hk, t);
+    int n = seq_steps<AT_WAVES>(a, s0 + lane, hk, t);
     if (s0 == 0) mine = n;
     if (a.seqs > 1)
 #pragma unroll
@@ -412,7 +412,7 @@ __global__ __launch_bounds__(at_waves(D) * 64, at_waves(D) / 4) void attend_stre
   int s = a.whole ? x : (a.seqs > 1 ? a.seqs : 0);
   int64_t g0 = a.whole ? x : 0;
   for (int s0 = 0; s0 < a.seqs && s == a.seqs; s0 += 64) {
-    const int n = s0 == 0 ? mine : seq_steps<D>(a, s0 + lane, hk, t);
+    const int n = s0 == 0 ? mine : seq_steps<AT_WAVES>(a, s0 + lane, hk, t);
     int sum = n;
 #pragma unroll
     for (int k = 1; k < 64; k *= 2) {
@@ -434,7 +434,7 @@ __global__ __launch_bounds__(at_waves(D) * 64, at_waves(D) / 4) void attend_stre
   const __amdgpu_buffer_rsrc_t part = pieces_of(a.part), part_ml = pieces_of(a.part_ml);
 
   for (; at < to && s < a.seqs; ++s) {
-    const int n = seq_steps<D>(a, s, hk, t);
+    const int n = seq_steps<AT_WAVES>(a, s, hk, t);
     if (n == 0) {
       at += a.whole;                              // (a share of its own)
       continue;
@@ -442,7 +442,7 @@ __global__ __launch_bounds__(at_waves(D) * 64, at_waves(D) / 4) void attend_stre
     const int off = (int)(at - g0), take = (int)(to - at < n - off ? to - at : n - off);
     const bool whole = take == n;
     const int c0 = t.beg + off * AT_STEP, c1 = off + take == n ? t.end : c0 + take * AT_STEP;
-    Piece<E, D, RT, Q8> p;
+    Piece<E, D, RT, Q8, AT_WAVES> p;
     p.run(a, t, c0, c1);
 
     // join the waves
@@ -540,7 +540,7 @@ __global__ __launch_bounds__(at_waves(D) * 64, at_waves(D) / 4) void attend_stre
   __syncthreads();
 #pragma unroll 1
   for (int k = 0; k < 2; ++k)
-    if (last_piece[k]) join_pieces<E, D>(a, piece_q0[k], piece_rows[k], hk, x0[k], x1[k], sums);
+    if (last_piece[k]) join_pieces<E, D, AT_WAVES>(a, piece_q0[k], piece_rows[k], hk, x0[k], x1[k], sums);
 }
 
 // Joins the splits of the tile kernel: four columns of a row are a thread's,
@@ -596,17 +596,20 @@ hipError_t join_launch(const AttendArgs& a, hipStream_t st) {
   return launch_kernel(attend_join_kernel<E, D>, dim3((unsigned)(tile_count(a, join_rows(D)) * a.kv.kv_heads)), 256, 0, st, a);
 }
 
-template <class E, int D, bool Q8>
-hipError_t stream_q(const AttendArgs& a, hipStream_t st) {
+template <class E, int D, bool Q8, int WAVES>
+hipError_t stream_w(const AttendArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)(a.shares * a.kv.kv_heads));
   if constexpr (D < 256)
-    if (a.stream_rows > 16) return launch_kernel(attend_stream_kernel<E, D, 2, Q8>, grid, at_waves(D) * 64, 0, st, a);
-  return launch_kernel(attend_stream_kernel<E, D, 1, Q8>, grid, at_waves(D) * 64, 0, st, a);
+    if (a.stream_rows > 16) return launch_kernel(attend_stream_kernel<E, D, 2, Q8, WAVES>, grid, WAVES * 64, 0, st, a);
+  return launch_kernel(attend_stream_kernel<E, D, 1, Q8, WAVES>, grid, WAVES * 64, 0, st, a);
 }
 
 template <class E, int D>
 hipError_t stream_d(const AttendArgs& a, hipStream_t st) {
-  return a.kv.k_scale ? stream_q<E, D, true>(a, st) : stream_q<E, D, false>(a, st);
+  if (!a.kv.k_scale) return stream_w<E, D, false, at_waves(D)>(a, st);
+  if constexpr (at_waves(D) != 4)
+    if (a.halved) return stream_w<E, D, true, 4>(a, st);
+  return stream_w<E, D, true, at_waves(D)>(a, st);
 }
 
 template <class E>
@@ -631,6 +634,7 @@ hipError_t launch_attend(const AttendArgs& args, const AttendPlan& p, int dtype,
   a.stream_rows = p.stream_rows;
   a.shares = p.splits;
   a.whole = p.whole;
+  a.halved = p.halved;
   if (a.fresh) {
     const int64_t wgs = (a.counters + 255) / 256;
     const hipError_t e = launch_kernel(zero_kernel, dim3((unsigned)(wgs < 1024 ? wgs : 1024)), 256, 0, st, a);

@@ -42,6 +42,11 @@ AttendPlan attend_plan(const AttendArgs& a, int num_cu) {
   p.splits = (int)(shares < 1 ? 1 : shares);
   p.whole = span(p.stream_rows, AT_TILE) <= 4 * at_step(D);
   if (p.whole) p.splits = a.seqs;
+  // Of 8 bits, more whole sequences than CUs in workgroups of 4 waves, two on a
+  // CU: one reads while the other begins or ends (64 sequences of 1000 keys, 8 key
+  // heads of 128: 34 us and 29; 256 of 704: 99 and 81; where there is a CU for each
+  // 8 waves are faster: 16 of 1000 13.1 us, and 15.2).
+  p.halved = a.kv.k_scale && p.whole && at_waves(D) == 8 && (int64_t)a.seqs * hk > num_cu;
   if (rows > most) {
     // All sequences are the tile kernel's where each has max_q rows (if cu_q
     // says so too), and where so few keys are seen that a tile of few rows ends

@@ -93,6 +93,7 @@ struct AttendArgs {
   int stream_rows;            // most rows of a streamed sequence; 0: none is streamed
   int shares;                 // workgroups of the streaming kernel for each key head
   bool whole;                 // each of them has a sequence of its own
+  bool halved;                // and has 4 waves (of 8 bits)
   uint32_t* arrived;          // [seqs][kv_heads] pieces of a sequence that are there; 0 between calls
   int64_t counters;           // entries of `arrived`
   bool fresh;                 // they are to be cleared first
@@ -112,6 +113,7 @@ struct AttendPlan {
   int stream_rows;            // most rows of a streamed sequence
   int splits;                 // shares of the streaming kernel
   bool whole;                 // of one sequence each
+  bool halved;                // by 4 waves instead of 8
   int tile_rows;              // rows of a workgroup of the tile kernel; 0: not launched
   int tile_splits, tile_per;
 };

@@ -261,6 +261,15 @@ def test_attend8_long_caches(gpu_lib, dtype, D, hk, G, kv, new, window):
     _attend8_case(dtype, D, 64 if new > 200 else 32, hk, G, [kv], [new], window=window, seed=kv)
 
 
+@pytest.mark.parametrize("dtype,D,hk,G,new,window", [(F16, 64, 1, 1, 1, 0), (BF16, 96, 2, 3, 1, 100), (BF16, 128, 1, 8, 3, 0), (F16, 128, 3, 2, 1, 0),
+                                                     (F16, 64, 1, 10, 2, 50)])
+def test_attend8_many_short_sequences(gpu_lib, dtype, D, hk, G, new, window):
+    # more sequences than CUs: workgroups of 4 waves
+    kvs = [1 + 37 * i % 211 for i in range(300)]
+    kvs[7], kvs[11], kvs[290] = 1000, 0, 513
+    _attend8_case(dtype, D, 16, hk, G, kvs, [min(new, max(k, 1)) for k in kvs], window=window, seed=D + G)
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16])
 def test_attend8_peaked_and_flat_scores(gpu_lib, dtype):
     _attend8_case(dtype, 64, 16, 1, 2, [900, 33], [3, 33], qscale=40.0, seed=1)

@@ -92,6 +92,30 @@ def test_large(gpu_lib, dtype):
         _case(dtype, 4, 131073, spread, seed=int(spread * 10), **kw)
 
 
+@pytest.mark.parametrize("rows", [1, 20, 130, 300])
+@pytest.mark.parametrize("dtype", [F16, F32])
+def test_parts(gpu_lib, dtype, rows):
+    """Rows whose tokens have to be read again, in as many parts as there are idle workgroups, and what a part finds too
+    large to hand over: sorted rows, whose tokens of a bin stand in one part, and rows of few different logits."""
+    tg = torch.Generator().manual_seed(rows)
+    few = min(rows, 6)
+    for vocab in (20000, 70001):
+        x = torch.randn((few, vocab), generator=tg) * 1.2
+        x = torch.cat([x.sort(dim=-1, descending=True)[0][:few // 2], x.sort(dim=-1)[0][few // 2:]])
+        ties = torch.randint(0, 5, (few, vocab), generator=tg).float()
+        for z in (x, ties):
+            z = z.to(dtype).cuda().repeat(-(-rows // few), 1)[:rows].contiguous()
+            u = torch.rand(few, generator=tg).cuda().repeat(-(-rows // few))[:rows].contiguous()
+            n = min(rows, 4)
+            for kw in ({}, {"top_p": 0.8}, {"top_k": 3000}, {"min_p": 0.05}, {"top_k": 9000, "top_p": 0.9, "min_p": 0.01}):
+                full = {k: torch.full((rows,), v, dtype=torch.int32 if k == "top_k" else F32, device="cuda") for k, v in kw.items()}
+                from gguf_quant_block_amd.serving import sample
+                lp = torch.empty(rows, device="cuda")
+                out = sample(z, u, logprobs=lp, **full)
+                _check(z[:n], u[:n], out[:n], lp[:n], **{k: v[:n] for k, v in full.items()})
+                assert all(torch.equal(out[i::few], out[i:i + 1].expand_as(out[i::few])) for i in range(few))
+
+
 def test_borders(gpu_lib):
     """Settings at their ends, random numbers at theirs, ties across borders."""
     inf, nan = float("inf"), float("nan")
