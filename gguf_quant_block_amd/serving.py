@@ -42,33 +42,40 @@ def _stream(index):
 
 
 # The checks of a call take most of its time on the host (an append of one
-# token: 13.6 us with messages formatted ahead of the checks, of which 4.3 are
-# the library's call), so they compare plain attributes and format a message
-# only to raise it.  A tensor's device is compared by its index (-1: not on a
-# GPU).
+# token: 13.6 us with messages formatted ahead of the checks, of which 4.2 are
+# the library's call; 8.3 without; 7.4 where nothing is asked of a tensor
+# twice), so they compare plain attributes and format a message only to raise
+# it.  A tensor's device is compared by its index (-1: not on a GPU).
 
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
 
 
+_INT32 = torch.int32
+
+
 def _heads(x, heads, dim, dtype, index, name):
-    """[T, heads, dim] whose heads and dimensions lie next to each other: its row stride."""
-    if x.dtype is not dtype or x.get_device() != index or x.dim() != 3:
+    """[T, heads, dim] whose heads and dimensions lie next to each other: its row stride, rows and heads."""
+    shape = x.shape
+    if x.dtype is not dtype or x.get_device() != index or len(shape) != 3:
         raise ValueError(f"{name}: a {dtype} tensor [T, heads, head_dim] on cuda:{index}")
-    t, h, d = x.shape
+    t, h, d = shape
     if d != dim or (heads is not None and h != heads):
         raise ValueError(f"{name}: [T, {heads or 'heads'}, {dim}], got {tuple(x.shape)}")
     row, head, one = x.stride()
     # strides of axes of length 0 or 1 say nothing
     if one != 1 or (head != d and h > 1):
         raise ValueError(f"{name}: heads and dimensions must be contiguous")
-    return row if t > 1 else max(row, h * d) // 8 * 8
+    return (row if t > 1 else max(row, h * d) // 8 * 8), t, h
 
 
 def _ints(x, index, name, dim=None):
-    if x.dtype is not torch.int32 or x.get_device() != index or not x.is_contiguous() or (dim is not None and x.dim() != dim):
+    """A contiguous int32 tensor: its shape."""
+    shape = x.shape
+    if x.dtype is not _INT32 or x.get_device() != index or not x.is_contiguous() or (dim is not None and len(shape) != dim):
         raise ValueError(f"{name}: a contiguous int32 tensor on cuda:{index}" + (f" of {dim} dimensions" if dim else ""))
+    return shape
 
 
 def _floats(x, n, index, name):
@@ -216,28 +223,25 @@ class PagedKv:
         slots i32 [T] (page * page_size + place; negative: not appended).  Returns
         the q so treated, in out (q itself, or None for a new tensor).  q may be None:
         keys and values only.  The three may be parts of one projection's rows."""
-        dev, dim, dtype = self.index, self.head_dim, self.dtype
-        t = k.shape[0]
-        ks = _heads(k, self.kv_heads, dim, dtype, dev, "k")
-        vs = _heads(v, self.kv_heads, dim, dtype, dev, "v")
-        _ints(slots, dev, "slots", 1)
-        if v.shape[0] != t or slots.shape[0] != t:
+        dev, dim, dtype, kv_heads = self.index, self.head_dim, self.dtype, self.kv_heads
+        ks, t, _ = _heads(k, kv_heads, dim, dtype, dev, "k")
+        vs, v_rows, _ = _heads(v, kv_heads, dim, dtype, dev, "v")
+        if v_rows != t or _ints(slots, dev, "slots", 1)[0] != t:
             raise ValueError("k, v and slots: one row for each token")
         kp, vp = k.data_ptr(), v.data_ptr()
         qp = op = None
         heads = qs = os = 0
         if q is not None:
-            qs = _heads(q, None, dim, dtype, dev, "q")
-            rows, heads, _ = q.shape
+            qs, rows, heads = _heads(q, None, dim, dtype, dev, "q")
             given = out is not None
             if not given:
                 out = torch.empty((t, heads, dim), dtype=dtype, device=self.device)
-            os = _heads(out, heads, dim, dtype, dev, "out")
-            if rows != t or out.shape[0] != t:
+            os, out_rows, _ = _heads(out, heads, dim, dtype, dev, "out")
+            if rows != t or out_rows != t:
                 raise ValueError("q and out: one row for each token")
             qp, op = q.data_ptr(), out.data_ptr()
             if given:
-                w, kw, n = 2 * heads * dim, 2 * self.kv_heads * dim, 2 * (t - 1)
+                w, kw, n = 2 * heads * dim, 2 * kv_heads * dim, 2 * (t - 1)
                 end = op + n * os + w                     # (most calls end at the comparisons of the whole ranges)
                 if qp < end and op < qp + n * qs + w and (qp != op or qs != os) and _overlap(op, 2 * os, w, qp, 2 * qs, w, t):
                     raise ValueError("out: q itself, or other memory")
@@ -246,9 +250,9 @@ class PagedKv:
                     raise ValueError("out: no memory of k or v")
         pp, axes, fp, ap, rot, inter, scale = None, 1, None, None, 0, 0, 1.0
         if rope is not None:
-            _need(positions is not None, "positions: needed with a rope")
-            _ints(positions, dev, "positions")
-            shape = positions.shape
+            if positions is None:
+                raise ValueError("positions: needed with a rope")
+            shape = _ints(positions, dev, "positions")
             if len(shape) == 2:
                 axes = shape[0]
             if len(shape) not in (1, 2) or shape[-1] != t:
@@ -258,7 +262,7 @@ class PagedKv:
             pp, fp, rot, inter, scale = positions.data_ptr(), rope.freq_ptr, rope.rot_dim, rope.interleaved, rope.scale
             ap = rope.axis_ptr
         if norm is None:
-            rc = _call("fc_gguf_kv_append")(self._h, qp, qs, heads, kp, ks, vp, vs, t, slots.data_ptr(), pp,
+            rc = (_calls.get("fc_gguf_kv_append") or _call("fc_gguf_kv_append"))(self._h, qp, qs, heads, kp, ks, vp, vs, t, slots.data_ptr(), pp,
                                             axes, fp, ap, rot, inter, scale, op, os, _stream(dev))
         else:
             if norm.index != dev:
@@ -280,16 +284,14 @@ class PagedKv:
         to fill, or None.  Returns the output, in out (None: a new tensor, zeros
         where no sequence has a row)."""
         dev, dim, dtype = self.index, self.head_dim, self.dtype
-        qs = _heads(q, None, dim, dtype, dev, "q")
-        t, heads, _ = q.shape
-        _ints(cu_q, dev, "cu_q", 1)
-        _ints(kv_lens, dev, "kv_lens", 1)
-        seqs = kv_lens.shape[0]
-        if cu_q.shape[0] != seqs + 1:
+        qs, t, heads = _heads(q, None, dim, dtype, dev, "q")
+        seqs = _ints(kv_lens, dev, "kv_lens", 1)[0]
+        if _ints(cu_q, dev, "cu_q", 1)[0] != seqs + 1:
             raise ValueError("cu_q: one entry more than kv_lens")
-        if table.dtype is not torch.int32 or table.get_device() != dev or table.dim() != 2 or table.shape[0] != seqs:
+        shape = table.shape
+        if table.dtype is not _INT32 or table.get_device() != dev or len(shape) != 2 or shape[0] != seqs:
             raise ValueError(f"table: an int32 tensor [seqs, pages] on cuda:{dev}")
-        width = table.shape[1]
+        width = shape[1]
         ts, one = table.stride()
         if one != 1 and width > 1:
             raise ValueError("table: contiguous rows")
@@ -300,8 +302,8 @@ class PagedKv:
         given = out is not None
         if not given:
             out = torch.zeros((t, heads, dim), dtype=dtype, device=self.device)
-        os = _heads(out, heads, dim, dtype, dev, "out")
-        if out.shape[0] != t:
+        os, out_rows, _ = _heads(out, heads, dim, dtype, dev, "out")
+        if out_rows != t:
             raise ValueError("out: one row for each token")
         qp, op = q.data_ptr(), out.data_ptr()
         w = 2 * heads * dim
