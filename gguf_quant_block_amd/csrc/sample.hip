@@ -627,7 +627,7 @@ struct RowChoice {
       // (at first the ends hold what is outside the range too)
       const u64 from = lo + ((u64)w << shift), to = shift ? from + (((u64)1 << shift) - 1) : from;
       lo = first && w == 0 ? 0 : from;
-      hi = first && w == (int)(range >> shift) ? ~0ull : to;
+      hi = first && w == (int)(range >> shift) ? ~0ull : to < hi ? to : hi;   // (the last way may reach past the range)
       if (lo >> 32 == hi >> 32) {              // one logit: ids below vocab
         const u64 most = (lo >> 32) << 32 | (uint64_t)(a.vocab - 1);
         if (hi > most) hi = most;

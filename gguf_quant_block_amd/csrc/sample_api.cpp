@@ -10,6 +10,7 @@
 namespace {
 
 constexpr int64_t kMaxRows = 65535, kMaxVocab = (int64_t)1 << 24;
+constexpr int64_t kMaxSlices = (int64_t)1 << 23;      // a launch has under 2^32 threads: 512 for each
 
 bool on(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -42,7 +43,8 @@ int64_t fc_gguf_sample_workspace(int64_t rows, int64_t vocab) {
   if (rows > kMaxRows || vocab > kMaxVocab) return FC_GGUF_ERANGE;
   const int cus = fcg::cus_of_current();
   if (cus <= 0) return FC_GGUF_EHIP;
-  return (int64_t)Division(rows, vocab, cus).bytes;
+  const Division d(rows, vocab, cus);
+  return rows * d.slices < kMaxSlices ? (int64_t)d.bytes : FC_GGUF_ERANGE;
 }
 
 int fc_gguf_sample(const void* x, int64_t x_stride, int dtype, int64_t rows, int64_t vocab, const float* u,
@@ -59,6 +61,7 @@ int fc_gguf_sample(const void* x, int64_t x_stride, int dtype, int64_t rows, int
   const int cus = fcg::cus_of_current();
   if (cus <= 0) return FC_GGUF_EHIP;
   const Division d(rows, vocab, cus);
+  if (rows * d.slices >= kMaxSlices) return FC_GGUF_ERANGE;
   if (workspace_bytes < 0 || (size_t)workspace_bytes < d.bytes) return FC_GGUF_EINVAL;
   fcg::SampleArgs a = {};
   a.slice = d.slice;

@@ -116,6 +116,21 @@ def test_parts(gpu_lib, dtype, rows):
                 assert all(torch.equal(out[i::few], out[i:i + 1].expand_as(out[i::few])) for i in range(few))
 
 
+@pytest.mark.parametrize("dtype", [F16, F32])
+@pytest.mark.parametrize("temperature", [4.0, 30.0, 1e4])
+def test_bins_about_zero(gpu_lib, dtype, temperature):
+    """Wide bins about 0, where logits stand many exponents apart, are taken apart over several levels."""
+    tg = torch.Generator().manual_seed(int(temperature))
+    for vocab, spread in ((2048, 0.73), (5000, 0.05), (40000, 1.0)):
+        x = torch.randn((60, vocab), generator=tg) * spread * 10.0 ** (torch.randn((60, vocab), generator=tg) * 0.5)
+        x, u = x.to(dtype).cuda(), torch.rand(60, generator=tg).cuda()
+        t = torch.full((60,), temperature, device="cuda")
+        for kw in ({}, {"top_p": torch.full_like(t, 0.9)}, {"top_k": _i32([vocab // 3] * 60)}, {"min_p": torch.full_like(t, 0.8)}):
+            out, lp = _run(x, u, temperature=t, **kw)
+            again, _ = _run(x, u, temperature=t, **kw)
+            assert torch.equal(out, again)
+
+
 def test_borders(gpu_lib):
     """Settings at their ends, random numbers at theirs, ties across borders."""
     inf, nan = float("inf"), float("nan")
