@@ -30,6 +30,10 @@
 // (serving.h).  Both need a value of a whole head: its units stand in
 // neighbouring lanes of a wave (of 96 dimensions 6 of 8), which exchange sums
 // and maxima; of a run of V the largest of each of its 8 tokens.
+// Measured, 4096 tokens of 32 query and 8 key heads of 128: with norms 22.3 us
+// (101 MB, 4.5 TB/s: what the plain rotation takes), into 8 bits 22.2 (92 MB, 4.2
+// TB/s, with HBM writing 47.7 of 41.9 MB, for cache lines that several workgroups
+// fill); 128 tokens of a batch, norms and 8 bits, 6.8; one token with norms 4.6.
 #include "serving.h"
 
 namespace fcg {

@@ -22,6 +22,16 @@
 // tokens are few, as they mostly are, is not read again.  Where it has to be,
 // for the bins in which something ends, the workgroups that the rows leave idle
 // read parts of it, and the one that is done last goes on with what they found.
+//
+// Measured, kernels alone: a row of 32064 with top_k, top_p and min_p 4.8 us and
+// 11.3; 128 rows of 131073 f32 with top_p 24.0 and 18.9, where 67 MB are read
+// once (2.8 TB/s) by 24 us of which reading is 13, weights and additions in LDS 6
+// and first tokens 5; 33 rows of 131072 bf16, nearly flat, two thirds hidden 11.3
+// and 33.6, where the rows are read again.  The second kernel is bound by latency:
+// joining 17 histograms, running sums, ranks, each behind a barrier.
+// Rows whose ends fall in bins of more than LIST tokens are read by one workgroup
+// several times: 131073 logits about 0 with a deviation of 0.1 145 us, with top_p
+// 211; 131073 equal ones 370 and 727.
 #include <math.h>
 
 #include "serving.h"
@@ -508,9 +518,10 @@ struct RowChoice {
   }
 
   // f(x, id, M) of every token of a bin: from the list, into which its tokens go
-  // if they fit it, or from the row
+  // if they fit it, or from the row, where those whose place in the order is
+  // outside [lo, hi] may be passed over (their bin and M take 30 instructions)
   template <class F>
-  __device__ __forceinline__ void each_of(int bin, F f) {
+  __device__ __forceinline__ void each_of(int bin, u64 lo, u64 hi, F f) {
     if (holds(bin)) {
       for (int i = tid; i < list_n; i += THREADS) {
         const u64 o = s.list[i];
@@ -520,7 +531,9 @@ struct RowChoice {
       }
       return;
     }
-    const float low = lowest_of(bin, top, top_q, set.c4).out, high = bin == 0 ? INFINITY : lowest_of(bin - 1, top, top_q, set.c4).in;
+    // (an end of the order that no logit has is a NaN, which fmaxf and fminf leave out)
+    const float low = fmaxf(lowest_of(bin, top, top_q, set.c4).out, logit_of(hi));
+    const float high = fminf(bin == 0 ? INFINITY : lowest_of(bin - 1, top, top_q, set.c4).in, logit_of(lo));
     each_above(0, a.vocab, low, [&](float v, uint32_t id) {
       u64 m;
       if (v <= high && bin_of(v, m) == bin) f(v, id, m);
@@ -576,13 +589,28 @@ struct RowChoice {
         s.part_count[tid] = 0;
       }
       __syncthreads();
-      each_of(bin, [&](float v, uint32_t id, u64 m) {
+      // A thread adds up while the way stays the same: 131073 equal logits went to one
+      // counter one by one, 250 us a pass.
+      int way = 0;
+      u64 way_sum = 0;
+      uint32_t way_count = 0;
+      auto put = [&]() {
+        if (!way_count) return;
+        atomicAdd(&s.part_sum[way], way_sum);
+        atomicAdd(&s.part_count[way], way_count);
+        way_sum = 0;
+        way_count = 0;
+      };
+      each_of(bin, first ? 0 : lo, first ? ~0ull : hi, [&](float v, uint32_t id, u64 m) {
         const u64 o = order_of(v, id);
         if (!first && (o < lo || o > hi)) return;
         const int w = o < lo ? 0 : o > hi ? (int)(range >> shift) : (int)((o - lo) >> shift);
-        atomicAdd(&s.part_sum[w], m);
-        atomicAdd(&s.part_count[w], 1u);
+        if (w != way) put();
+        way = w;
+        way_sum += m;
+        ++way_count;
       });
+      put();
       __syncthreads();
       if (tid < 64) {
         // running sums, four ways a lane
@@ -642,7 +670,7 @@ struct RowChoice {
       s.few_rank[tid] = 0;
     }
     __syncthreads();
-    each_of(bin, [&](float v, uint32_t id, u64 m) {
+    each_of(bin, lo, hi, [&](float v, uint32_t id, u64 m) {
       const u64 o = order_of(v, id);
       if (o < lo || o > hi) return;
       const uint32_t i = atomicAdd(&s.n, 1u);
@@ -979,7 +1007,7 @@ struct RowChoice {
       __syncthreads();
       uint32_t c = 0;
       u64 m = 0;
-      each_of(least_bin, [&](float v, uint32_t, u64 w) {
+      each_of(least_bin, 0, ~0ull, [&](float v, uint32_t, u64 w) {
         if ((double)v >= least) {
           ++c;
           m += w;

@@ -203,8 +203,9 @@ struct SampleArgs {
   int slice, slices;          // tokens of a slice, slices of a row
   int row_parts;              // workgroups that choose a row's token
 };
-// Tokens of a slice: few where larger ones would leave CUs idle.  (128 rows of
-// 131073 f32, both launches: slices of 4096 59 us, of 8192 52, of 16384 54.)
+// Tokens of a slice: few where larger ones would leave CUs idle.  (Both launches,
+// slices of 4096 and of 8192: 128 rows of 131073 f32 50.0 us and 43.1; a row of
+// 32064 16.0 and 16.0, of which the first launch 4.8 and 5.4.)
 inline int sample_slice(int64_t rows, int64_t vocab, int num_cu) {
   return rows * ((vocab + 8191) / 8192) < 2 * (int64_t)num_cu ? 4096 : 8192;
 }

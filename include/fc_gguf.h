@@ -482,8 +482,9 @@ int fc_gguf_logits(const void* x, int64_t x_stride, int dtype, int64_t rows, int
  * Weights are rounded to whole numbers (by 2^-33 of themselves at most) and
  * summed as such, so that a row's result depends on that row alone and equal
  * calls give equal bits.  rows <= 65535, vocab <= 2^24 and rows times the slices
- * of 8192 tokens that a row has under 2^23 (else ERANGE); rows == 0 is a no-op.  Runs on the current
- * device.  out and logprobs must not overlap the inputs or the workspace.
+ * of 8192 tokens that a row has under 2^23 (else ERANGE); rows == 0 is a no-op.
+ * Runs on the current device.  out and logprobs must not overlap the inputs or
+ * the workspace.
  */
 int fc_gguf_sample(const void* x, int64_t x_stride, int dtype, int64_t rows, int64_t vocab, const float* u,
                    const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,

@@ -131,6 +131,20 @@ def test_bins_about_zero(gpu_lib, dtype, temperature):
             assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("vocab", [4097, 33001, 131073])
+def test_logits_next_to_each_other(gpu_lib, vocab):
+    """Equal logits, and f32 steps from 1: the ids, or the last bits, say what the order is.  131073 steps of 2^-23 are 2^-6:
+    weights differ by 1.6 %, and the share of the first k tokens from k / vocab by less."""
+    u = _f32([0.0, 0.1, 0.5, 0.77, 0.999])
+    equal = torch.full((5, vocab), 0.25, device="cuda")
+    steps = torch.arange(vocab, dtype=torch.float64).mul(2.0**-23).add(1.0).float().flip(0).repeat(5, 1).cuda()
+    for x in (equal, steps):
+        for kw in ({}, {"top_p": _f32([0.3] * 5)}, {"top_k": _i32([vocab // 2] * 5)}):
+            out, _ = _run(x, u, **kw)
+            part = 0.3 if "top_p" in kw else 0.5 if "top_k" in kw else 1.0
+            assert ((out.double() / vocab - u.double() * part).abs() < 2.0**-5 + 2 / vocab).all()
+
+
 def test_borders(gpu_lib):
     """Settings at their ends, random numbers at theirs, ties across borders."""
     inf, nan = float("inf"), float("nan")
