@@ -48,11 +48,13 @@ namespace {
 // of the second dimension 32 (d / 2) + 2r + d % 2.  A lane still ends with the
 // scores of keys 8g .. 8g + 7, in another order.  Codes become values of E
 // where they are used, exactly (serving.h): what follows is the same.
+//
 // Measured: 64 tokens over up to 8192 keys each 81 us (372 MB, 4.6 TB/s; of 16
-// bits 137); one token over 131072 keys 56.4 with pages that were not read lately
-// (270 MB, 4.8 TB/s; 49 with, of 16 bits 98): the codes of half the bytes leave
-// less in flight.  8 x 5 drafted tokens over up to 6001 keys 26 us, one over
-// 1003 keys 9.6.
+// bits 137); about 12 us of it are the call's begin and end and 10 the changes
+// from sequence to sequence, and longer caches come to 6.1 TB/s.  One token over
+// 131072 keys 56.4 us, or 49 with pages that the last-level cache holds in part
+// (270 MB; of 16 bits 98); 8 x 5 drafted tokens over up to 6001 keys 26, one over
+// 1003 keys 9.6.  A second tile in flight gained nothing (85 us instead of 82).
 template <class E, int D, int RT, bool Q8, int WAVES>
 struct Piece {
   static constexpr int KS = D / 32, DT = D / 16, AT_STEP = WAVES * AT_TILE;
