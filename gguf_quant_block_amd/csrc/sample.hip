@@ -27,7 +27,7 @@
 // 11.3; 128 rows of 131073 f32 with top_p 24.0 and 18.9, where 67 MB are read
 // once (2.8 TB/s) by 24 us of which reading is 13, weights and additions in LDS 6
 // and first tokens 5; 33 rows of 131072 bf16, nearly flat, two thirds hidden 11.3
-// and 33.6, where the rows are read again.  The second kernel is bound by latency:
+// and 34.2, where the rows are read again.  The second kernel is bound by latency:
 // joining 17 histograms, running sums, ranks, each behind a barrier.
 // Rows whose ends fall in bins of more than LIST tokens are read by one workgroup
 // several times: 131073 logits about 0 with a deviation of 0.1 145 us, with top_p
