@@ -34,6 +34,8 @@
 // (101 MB, 4.5 TB/s: what the plain rotation takes), into 8 bits 22.2 (92 MB, 4.2
 // TB/s, with HBM writing 47.7 of 41.9 MB, for cache lines that several workgroups
 // fill); 128 tokens of a batch, norms and 8 bits, 6.8; one token with norms 4.6.
+#include <type_traits>
+
 #include "serving.h"
 
 namespace fcg {
@@ -143,6 +145,40 @@ __device__ __forceinline__ int quantise16(const float* x, uint32_t* code) {
     code[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2], y[4 * i + 3], lo, true);
   }
   return e;
+}
+
+// The mean square of a head, of which x are this lane's 16 values, and eps, whose
+// root norms the head.  Squares of f16 are well inside the range of f32.  Those of
+// bf16 are not from 2^64 on, nor are they precise below 2^-63: such a head, and
+// eps with it, is first scaled by the power of two that takes the larger of its
+// values and the root of eps below 1.  The scaled values have the same norm, and
+// other heads keep their bits.  (A head with an infinite value, or of zeros without
+// eps, stays what it is: by the formula NaN.)  The question costs 4096 bf16 tokens of
+// 32 query and 8 key heads of 128 0.3 to 0.5 of 21.6 us.
+template <class E, int LANES>
+__device__ __forceinline__ float mean_square(float* x, float one_of, float eps) {
+  auto mean = [&](float e) -> float {
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) sum = fmaf(x[j], x[j], sum);
+    return sum_lanes<LANES>(sum) * one_of + e;
+  };
+  float y = mean(eps);
+  if constexpr (std::is_same<E, bf16>::value) {
+    // (a mean of 2^-100: what squares lose below f32's normal range, 2^-150 each, is nothing to it)
+    const bool odd = !(y >= 0x1p-100f && y < INFINITY);
+    if (__any(odd)) {
+      float m = 0.f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(x[j]));
+      m = fmaxf(max_lanes<LANES>(m), sqrtf(eps));
+      const int by = odd && m > 0.f && m < INFINITY ? -__builtin_amdgcn_frexp_expf(m) : 0;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[j] = __builtin_ldexpf(x[j], by);
+      y = mean(__builtin_ldexpf(eps, 2 * by));
+    }
+  }
+  return y;
 }
 
 // A unit of 16 elements of a head: where it comes from and where it goes.
@@ -340,10 +376,7 @@ __global__ __launch_bounds__(AP_THREADS) void kv_append_kernel(AppendArgs a) {
         const bool isq = z.h < a.q_heads;
         const float* weight = isq ? a.q_norm + (int64_t)z.h * a.q_norm_stride : a.k_norm + (int64_t)(z.h - a.q_heads) * a.k_norm_stride;
         if (isq ? a.q_norm != nullptr : a.k_norm != nullptr) {
-          float sum = 0.f;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) sum = fmaf(x[j], x[j], sum);
-          const float by = 1.f / sqrtf(sum_lanes<lanes>(sum) * (1.f / D) + a.eps);
+          const float by = 1.f / sqrtf(mean_square<E, lanes>(x, 1.f / D, a.eps));
           if (lanes == units || z.u < units) {
             float g[16];
 #pragma unroll

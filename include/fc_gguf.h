@@ -375,7 +375,8 @@ int fc_gguf_kv_append(fc_gguf_kv_t h, const void* q, int64_t q_stride, int q_hea
  * fc_gguf_kv_append with norms of queries and keys for each head ahead of the
  * rotation:
  *   x = x / sqrt(mean of x^2 over the head + eps) * weight
- * in f32, and one rounding after the rotation.
+ * in f32, and one rounding after the rotation.  Heads of any finite values: of
+ * bf16 ones whose squares leave f32's range the mean is taken of scaled values.
  *   q_norm, k_norm  device f32 [head_dim] (stride 0), or [q_heads | kv_heads]
  *                   [head_dim] (stride head_dim), 16-byte aligned, or NULL: no
  *                   norm of these (both NULL: fc_gguf_kv_append)
