@@ -137,6 +137,7 @@ __device__ __forceinline__ Settings settings_of(const SampleArgs& a, int64_t row
   if (s.top_k < 0) s.top_k = 0;
   if (!(s.top_p < 1.0)) s.top_p = 1.0;
   if (!(t > 0.f) || s.top_p <= 0.0 || s.min_p > 1.0) s.top_k = 1;
+  if (t == INFINITY) s.min_p = 0.0;            // (all finite logits weigh 1, however far below the top)
   if (s.top_k == 1) {
     s.top_p = 1.0;
     s.min_p = 0.0;
