@@ -404,11 +404,12 @@ _workspaces = {}                                           # bytes that (device,
 
 def sample(x, u, *, temperature=None, top_k=None, top_p=None, min_p=None, out=None, logprobs=None):
     """The next token of each row of logits x [rows, vocab] (f16, bf16 or f32; rows may be strided) from random numbers
-    u f32 [rows] in [0, 1).  Of the tokens in decreasing order (ties by lowest id) the first top_k i32 [rows] are kept (0:
-    all), of these the shortest beginning that holds top_p f32 [rows] of their weight, of these the ones whose weight is
-    at least min_p f32 [rows] of the largest's; weights are exp(x / temperature), temperature f32 [rows] (1; 0: the
-    largest token).  Masked tokens (-inf) and NaN take no part; a row where nothing does gives -1.  Returns the ids in out i32 [rows]
-    (None: a new tensor); logprobs f32 [rows], to fill: the log of the chosen token's share of the kept weight, or None."""
+    u f32 [rows] in [0, 1) (1 and more: a number just below).  Of the tokens in decreasing order (ties by lowest id) the
+    first top_k i32 [rows] are kept (0: all), of these the shortest beginning that holds top_p f32 [rows] of their weight,
+    of these the ones whose weight is at least min_p f32 [rows] of the largest's; weights are exp(x / temperature),
+    temperature f32 [rows] (1; 0: the largest token).  Masked tokens (-inf) and NaN take no part; a row where nothing does
+    gives -1.  Returns the ids in out i32 [rows] (None: a new tensor); logprobs f32 [rows], to fill: the log of the chosen
+    token's share of the kept weight, or None."""
     dev, dtype = x.get_device(), DTYPES.get(x.dtype)
     if dev < 0 or dtype is None or x.dim() != 2:
         raise ValueError("x: f16, bf16 or f32 [rows, vocab] on the GPU")

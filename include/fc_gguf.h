@@ -466,7 +466,8 @@ int fc_gguf_logits(const void* x, int64_t x_stride, int dtype, int64_t rows, int
  *            holds at least top_p of their weight; of these the tokens with
  *            w_v >= min_p; but always the first
  *   chosen   the first of the kept, in that order, whose running sum of weights
- *            is greater than u times their sum (u >= 1: the last)
+ *            is greater than u times their sum (u >= 1 counts as 1 - 2^-52: the last
+ *            of those that hold more than about that share of the sum)
  *   x            device [rows][vocab] of dtype (F16, BF16 or F32), row stride in
  *                elements; -inf and NaN take no part, +inf leaves only its like
  *   u            device f32[rows], in [0, 1) (below 0 or NaN: 0)
@@ -482,10 +483,11 @@ int fc_gguf_logits(const void* x, int64_t x_stride, int dtype, int64_t rows, int
  *                bytes at least, for this call alone until it is done
  * Weights are rounded to whole numbers (by 2^-33 of themselves at most) and
  * summed as such, so that a row's result depends on that row alone and equal
- * calls give equal bits.  rows <= 65535, vocab <= 2^24 and rows times the slices
- * of 8192 tokens that a row has under 2^23 (else ERANGE); rows == 0 is a no-op.
- * Runs on the current device.  out and logprobs must not overlap the inputs or
- * the workspace.
+ * calls give equal bits.  Tokens whose weight is under 2^-63.75 of the largest
+ * may count as -inf, and do under 2^-64.25.  rows <= 65535, vocab <= 2^24 and
+ * rows times the slices of 8192 tokens that a row has under 2^23 (else ERANGE);
+ * rows == 0 is a no-op.  Runs on the current device.  out and logprobs must not
+ * overlap the inputs or the workspace.
  */
 int fc_gguf_sample(const void* x, int64_t x_stride, int dtype, int64_t rows, int64_t vocab, const float* u,
                    const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,

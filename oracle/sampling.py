@@ -36,7 +36,7 @@ def choose(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
         margin = min(margin, np.abs(w[1:n + 1] / min_p - 1).min() if len(w) > 1 else 1.0)
         n = max(1, min(n, m))
     c = np.cumsum(w[:n])
-    u = u if u > 0 else 0.0
+    u = min(u, 1 - 2.0 ** -52) if u > 0 else 0.0
     t = u * c[-1]
     if u > 0:
         margin = min(margin, np.abs(c[:-1] - t).min() / c[-1] if n > 1 else 1.0)

@@ -5,6 +5,8 @@ import math
 import pytest
 import torch
 
+from oracle import sampling as o
+
 pytestmark = pytest.mark.gpu
 F32 = torch.float32
 
@@ -43,3 +45,27 @@ def test_infinite_temperature_beside_ends_of_min_p(gpu_lib):
     assert out.tolist() == [0, 0, 2]
     x[:, 1] = inf                                                # an infinite logit leaves only its like, at any temperature
     assert sample(x, _f32([0.9] * 3), temperature=_f32([inf] * 3), min_p=_f32([1.0, 0.5, 0.0])).tolist() == [1, 1, 1]
+
+
+def test_numbers_of_one_and_more(gpu_lib):
+    """They count as 1 - 2^-52: a last token that holds less of the sum than 2^-52 is not chosen, and one that weighs less
+    than 2^-64 of the largest never is."""
+    from gguf_quant_block_amd.serving import sample
+    rows = [[0.0, -30.0], [0.0, -40.0], [0.0, -100.0], [2.0, 2.0], [-100.0, 0.0], [1.0, -math.inf], [0.0, -1e30]]
+    want = [1, 0, 0, 1, 1, 0, 0]
+    for v in (1.0, 1.5, math.inf):
+        out = sample(_f32(rows), _f32([v] * len(rows)))
+        assert out.tolist() == want
+        assert [o.choose(r, v)[0] for r in rows] == want
+    # rows of many tokens, which are taken apart by bins; the last of equal ones is the last id
+    x = torch.zeros((2, 20000), device="cuda")
+    x[1, :10000] = -100.0
+    for v in (1.0, 7.0):
+        assert sample(x, _f32([v, v])).tolist() == [19999, 19999]
+    x[1] = 0
+    x[1, 15000:] = -100.0
+    assert sample(x, _f32([1.0, 1.0])).tolist() == [19999, 14999]
+    # the kept tokens end before: the last of them
+    x = torch.arange(20000, device="cuda").flip(0).float()[None] / 20000
+    for k in (1, 7, 600, 9000):
+        assert sample(x, _f32([1.0]), top_k=torch.tensor([k], dtype=torch.int32, device="cuda")).tolist() == [k - 1]
