@@ -33,7 +33,10 @@
 // Measured, 4096 tokens of 32 query and 8 key heads of 128: with norms 22.3 us
 // (101 MB, 4.5 TB/s: what the plain rotation takes), into 8 bits 22.2 (92 MB, 4.2
 // TB/s, with HBM writing 47.7 of 41.9 MB, for cache lines that several workgroups
-// fill); 128 tokens of a batch, norms and 8 bits, 6.8; one token with norms 4.6.
+// fill); 128 tokens of a batch, norms and 8 bits, 6.9; one token with norms 4.5.
+// Heads of 96 with norms or in 8 bits are further from that: the compiler keeps a
+// unit that not every lane has in 48 bytes of scratch memory.  4096 tokens with
+// norms 26.5 us (16.4 without; a copy of the bytes 16.2), into 8 bits 25 (14.9).
 #include <type_traits>
 
 #include "serving.h"

@@ -284,7 +284,7 @@ int fc_gguf_debug_weights(fc_gguf_t h, void* dst, void* stream);
 /* Element types. */
 #define FC_GGUF_F16  0
 #define FC_GGUF_BF16 1
-#define FC_GGUF_F32  2   /* logits only */
+#define FC_GGUF_F32  2   /* logits that are processed or sampled */
 
 typedef struct fc_gguf_kv* fc_gguf_kv_t;
 
@@ -414,7 +414,7 @@ int fc_gguf_kv_append_norm(fc_gguf_kv_t h, const void* q, int64_t q_stride, int 
  * by T, max_q and table_width, which the host knows; lengths are read on the
  * device, so a captured graph may be replayed with other lengths within them.
  * Sums are f32, of weights up to 2^12 with bf16: keys' values past 2^100 may
- * make them infinite.
+ * make them infinite, or NaN where both signs occur.
  * The order of summation depends on sizes and lengths only: equal calls give
  * equal bits.  Limits (else FC_GGUF_ERANGE): T, max_q, window and table_width *
  * page_size <= 2^30, seqs <= 65535, and, with g = q_heads / kv_heads,
